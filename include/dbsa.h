@@ -295,6 +295,115 @@ dbsa_status dbsa_gather_rope_attend_noalloc(
     int64_t dbg_cap, void *stream);
 
 /* ---------------------------------------------------------------------------
+ * Paged cache and shared-prefix attention.
+ *
+ * The fixed-ICL setting of [DBSA notes] (every query attends to the whole
+ * demonstration set) in its serving form: the demonstrations are one prefix
+ * that all sequences of a batch share, and each sequence's own tokens (prompt
+ * and generated) live in fixed-size pages, so that sequences of different
+ * lengths grow and leave without moving each other.
+ *
+ * A cache is a pool of n_pages pages.  Token r of page p and KV head c is the
+ * head_dim contiguous elements at (p * page_stride + (c * page_size + r) *
+ * head_dim) of k_pages (keys, ROTATED at their positions) and of v_pages.  A
+ * page table is a list of page ids: entry j holds tokens [j * page_size,
+ * (j + 1) * page_size) of its sequence.  An entry outside [0, n_pages) (-1 by
+ * convention) means that the page is not there: its tokens are not attended
+ * to and nothing is appended to them.
+ *
+ * The arrays of a batch are DEVICE arrays, read by the kernels: a call can be
+ * captured into a CUDA graph and replayed after they have changed.  Their
+ * contents are not checked on the host; the kernels check every index:
+ *  - rows [row_ptr[s], row_ptr[s+1]) of the batch belong to sequence s; row_ptr
+ *    must not decrease.  A sequence whose rows are not inside [0, n_rows] has
+ *    no rows.  Rows of no sequence are ignored, and their outputs left as
+ *    they were.
+ *  - seq_lens[s] counts the own tokens of sequence s, its rows of this call
+ *    included: row i of n stands for own token t = seq_lens[s] - n + i.  Rows
+ *    with t < 0 are padding: nothing is appended for them, their output is 0.
+ *    A length outside [0, table_width * page_size] counts as 0.
+ * Own token t of a sequence sits at position pos0 + t (append) or prefix_len
+ * + t (attention).
+ *
+ * Both calls read RoPE angle tables that dbsa_rope_tables() has written once
+ * for cfg (its head_dim and rope_theta); they must cover every position a call
+ * can reach, pos0 (prefix_len) + table_width * page_size.
+ * ------------------------------------------------------------------------ */
+typedef struct dbsa_paged_cache {
+    void *k_pages, *v_pages; /* device, 16-byte aligned, cfg->dtype */
+    int64_t page_stride;     /* elements between pages: a multiple of 8, at
+                                least n_kv_heads * page_size * head_dim */
+    int32_t n_pages;         /* >= 1 */
+    int32_t page_size;       /* tokens: 16, 32, 64, 128 or 256 */
+} dbsa_paged_cache;
+
+typedef struct dbsa_paged_batch {
+    int32_t n_seqs;            /* 1..65535 */
+    int32_t n_rows;            /* rows of the call's q / k / v / out, >= 1 */
+    const int32_t *row_ptr;    /* device, [n_seqs + 1] */
+    const int32_t *seq_lens;   /* device, [n_seqs] */
+    const int32_t *page_table; /* device, row s at page_table + s * table_stride */
+    int32_t table_width;       /* entries per sequence, >= 1 */
+    int32_t table_stride;      /* >= table_width */
+} dbsa_paged_batch;
+
+/* Bytes of the angle tables for positions [0, n_pos), 0 on bad arguments; and
+ * the kernel that fills them (`tables`: device, 16-byte aligned). */
+size_t dbsa_rope_tables_size(const dbsa_config *cfg, int64_t n_pos);
+dbsa_status dbsa_rope_tables(const dbsa_config *cfg, int64_t n_pos, void *tables,
+                             size_t tables_bytes, void *stream);
+
+/* Appends the rows of a batch to their sequences' pages: the key of own token
+ * t rotated at position pos0 + t and rounded once to cfg->dtype, the value bit
+ * for bit.
+ *   k, v   device, pre-RoPE: row r, head c at r * row_stride + c * head_stride
+ *          elements (strides: multiples of 8, k and v each their own), so that
+ *          slices of a fused projection and the head-major Stage-1 cache
+ *          (row_stride = head_dim, head_stride = cap * head_dim) can both be
+ *          the source.  They may not overlap the pages.
+ * A slot named by two rows of one call ends up with either one's values.
+ * Needs no workspace.
+ * Errors: INVALID_ARG (null or misaligned pointer, bad sizes or strides,
+ * tables too small for the positions), UNSUPPORTED (cfg, page_size), CUDA. */
+dbsa_status dbsa_paged_append(const dbsa_config *cfg, const void *k, int64_t k_row_stride,
+                              int64_t k_head_stride, const void *v, int64_t v_row_stride,
+                              int64_t v_head_stride, const dbsa_paged_cache *cache,
+                              const dbsa_paged_batch *batch, int64_t pos0, const void *tables,
+                              size_t tables_bytes, void *stream);
+
+/* Attention of the rows of a batch over the shared prefix and, causally, their
+ * own sequences: row i (own token t, position prefix_len + t) attends to the
+ * prefix tokens 0 .. prefix_len - 1 and to own tokens 0 .. t, whose keys and
+ * values are in the cache already (dbsa_paged_append before it, on the same
+ * stream).  Each prefix page is read once per 128 query rows of a KV head,
+ * whatever the number of sequences.
+ *   q            device, pre-RoPE: row r, head h at r * q_row_stride + h *
+ *                head_dim (q_row_stride a multiple of 8)
+ *   prefix_pages device, [ceil(prefix_len / page_size)] page ids (may be NULL
+ *                when prefix_len is 0)
+ *   out          device, [n_rows][Hq][D]; rows that may attend to nothing
+ *                (padding, or every page missing) get 0
+ *   workspace    device, 256-byte aligned, ws_bytes >=
+ *                dbsa_shared_prefix_workspace_size(); its contents need not be
+ *                kept between calls.  Calls that may overlap on the GPU (other
+ *                streams, graphs replayed at once) need one each.
+ * Slots of a page at or past its sequence's length may hold anything, NaN
+ * included.  Keys and values of tokens inside a length must be finite.
+ * Results do not depend on what else is in the workspace, and repeat bit for
+ * bit.  DBSA_F32 caches are attended to in fp32; with DBSA_BF16 the rotated
+ * queries and the probabilities are rounded to bf16 for the tensor cores, and
+ * sums and softmax statistics are fp32.
+ * Errors: as dbsa_paged_append, and WORKSPACE. */
+size_t dbsa_shared_prefix_workspace_size(const dbsa_config *cfg, int32_t n_seqs, int32_t n_rows,
+                                         int64_t prefix_len);
+dbsa_status dbsa_shared_prefix_attend(const dbsa_config *cfg, const void *q,
+                                      int64_t q_row_stride, const dbsa_paged_cache *cache,
+                                      const int32_t *prefix_pages, int64_t prefix_len,
+                                      const dbsa_paged_batch *batch, const void *tables,
+                                      size_t tables_bytes, void *out, void *workspace,
+                                      size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
  * Status and introspection.
  * ------------------------------------------------------------------------ */
 

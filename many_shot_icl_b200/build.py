@@ -21,7 +21,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdbsa.so")
-SOURCES = ["dbsa_api.cu", "rope.cu", "stage1_attn.cu", "stage2_attn.cu", "noalloc.cu"]
+SOURCES = ["dbsa_api.cu", "rope.cu", "stage1_attn.cu", "stage2_attn.cu", "noalloc.cu",
+           "paged.cu", "paged_attn.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -27,27 +27,28 @@ thread_local cudaEvent_t g_prof_start = nullptr, g_prof_stop = nullptr;
 // nanoseconds (0: no hook).
 thread_local uint64_t g_wait_expiry_ns = 0;
 
+std::atomic<int64_t> g_launches{0};
+
+}  // namespace
+
+// ---- helpers shared with the other entry-point files (dbsa_internal.h) ----
+namespace dbsa {
+
 uint64_t take_wait_expiry() {
   const uint64_t w = g_wait_expiry_ns;
   g_wait_expiry_ns = 0;
   return w;
 }
-std::atomic<int64_t> g_launches{0};
 
 void count_launches(int n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
 
-// Records the profiling events (if any) around the main kernel of a call.
-struct ProfileScope {
-  cudaStream_t st;
-  cudaEvent_t stop;
-  explicit ProfileScope(cudaStream_t s) : st(s), stop(g_prof_stop) {
-    if (g_prof_start) cudaEventRecord(g_prof_start, st);
-    g_prof_start = g_prof_stop = nullptr;
-  }
-  ~ProfileScope() {
-    if (stop) cudaEventRecord(stop, st);
-  }
-};
+ProfileScope::ProfileScope(cudaStream_t s) : st(s), stop(g_prof_stop) {
+  if (g_prof_start) cudaEventRecord(g_prof_start, st);
+  g_prof_start = g_prof_stop = nullptr;
+}
+ProfileScope::~ProfileScope() {
+  if (stop) cudaEventRecord(stop, st);
+}
 
 dbsa_status fail(dbsa_status s, const char *fmt, ...) {
   char buf[512];
@@ -62,6 +63,54 @@ dbsa_status fail(dbsa_status s, const char *fmt, ...) {
 dbsa_status cuda_fail(cudaError_t e, const char *where) {
   return fail(DBSA_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
 }
+
+dbsa_status check_cfg(const dbsa_config *cfg) {
+  if (cfg == nullptr) return fail(DBSA_ERR_INVALID_ARG, "cfg is NULL");
+  if (cfg->n_q_heads <= 0 || cfg->n_kv_heads <= 0)
+    return fail(DBSA_ERR_INVALID_ARG, "head counts must be positive");
+  if (cfg->n_q_heads % cfg->n_kv_heads != 0)
+    return fail(DBSA_ERR_UNSUPPORTED, "n_q_heads must be a multiple of n_kv_heads");
+  if (cfg->n_q_heads / cfg->n_kv_heads > 64)
+    return fail(DBSA_ERR_UNSUPPORTED, "more than 64 query heads per KV head");
+  if (cfg->head_dim != 64 && cfg->head_dim != 128)
+    return fail(DBSA_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", cfg->head_dim);
+  if (cfg->dtype != DBSA_BF16 && cfg->dtype != DBSA_F32)
+    return fail(DBSA_ERR_UNSUPPORTED, "dtype must be DBSA_BF16 or DBSA_F32");
+  if (!(cfg->rope_theta > 1.0) || !std::isfinite(cfg->rope_theta))
+    return fail(DBSA_ERR_INVALID_ARG, "rope_theta must be a finite value > 1");
+  if (cfg->window_j < 0) return fail(DBSA_ERR_INVALID_ARG, "window_j must be >= 0");
+  if (cfg->pattern < 0 || cfg->pattern > 3) return fail(DBSA_ERR_INVALID_ARG, "unknown pattern");
+  if (cfg->reserved != 0) return fail(DBSA_ERR_INVALID_ARG, "reserved must be 0");
+  if (!std::isfinite(cfg->softmax_scale)) return fail(DBSA_ERR_INVALID_ARG, "bad softmax_scale");
+  return DBSA_OK;
+}
+
+float scale_log2(const dbsa_config *cfg) {
+  const double s = cfg->softmax_scale > 0.f ? (double)cfg->softmax_scale
+                                            : 1.0 / std::sqrt((double)cfg->head_dim);
+  return (float)(s * 1.4426950408889634);  // * log2(e)
+}
+
+int num_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return 148;
+  return n;
+}
+
+dbsa_status check_ws(void *ws, size_t ws_bytes, size_t need) {
+  if (ws == nullptr) return fail(DBSA_ERR_WORKSPACE, "workspace is NULL");
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return fail(DBSA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (ws_bytes < need)
+    return fail(DBSA_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+  return DBSA_OK;
+}
+
+}  // namespace dbsa
+
+namespace {
 
 constexpr size_t kAlign = 1024;
 // Block-major passes with at most this many query rows per (query, KV head)
@@ -235,27 +284,6 @@ struct Carve {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-dbsa_status check_cfg(const dbsa_config *cfg) {
-  if (cfg == nullptr) return fail(DBSA_ERR_INVALID_ARG, "cfg is NULL");
-  if (cfg->n_q_heads <= 0 || cfg->n_kv_heads <= 0)
-    return fail(DBSA_ERR_INVALID_ARG, "head counts must be positive");
-  if (cfg->n_q_heads % cfg->n_kv_heads != 0)
-    return fail(DBSA_ERR_UNSUPPORTED, "n_q_heads must be a multiple of n_kv_heads");
-  if (cfg->n_q_heads / cfg->n_kv_heads > 64)
-    return fail(DBSA_ERR_UNSUPPORTED, "more than 64 query heads per KV head");
-  if (cfg->head_dim != 64 && cfg->head_dim != 128)
-    return fail(DBSA_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", cfg->head_dim);
-  if (cfg->dtype != DBSA_BF16 && cfg->dtype != DBSA_F32)
-    return fail(DBSA_ERR_UNSUPPORTED, "dtype must be DBSA_BF16 or DBSA_F32");
-  if (!(cfg->rope_theta > 1.0) || !std::isfinite(cfg->rope_theta))
-    return fail(DBSA_ERR_INVALID_ARG, "rope_theta must be a finite value > 1");
-  if (cfg->window_j < 0) return fail(DBSA_ERR_INVALID_ARG, "window_j must be >= 0");
-  if (cfg->pattern < 0 || cfg->pattern > 3) return fail(DBSA_ERR_INVALID_ARG, "unknown pattern");
-  if (cfg->reserved != 0) return fail(DBSA_ERR_INVALID_ARG, "reserved must be 0");
-  if (!std::isfinite(cfg->softmax_scale)) return fail(DBSA_ERR_INVALID_ARG, "bad softmax_scale");
-  return DBSA_OK;
-}
-
 dbsa_status check_offs(const int32_t *offs, int32_t nb) {
   if (offs == nullptr) return fail(DBSA_ERR_INVALID_ARG, "offs is NULL");
   if (nb < 1) return fail(DBSA_ERR_INVALID_ARG, "need at least one block (nb = %d)", nb);
@@ -265,20 +293,6 @@ dbsa_status check_offs(const int32_t *offs, int32_t nb) {
       return fail(DBSA_ERR_INVALID_ARG, "block %d is empty or offsets decrease", b);
   if (offs[nb] > (1 << 30)) return fail(DBSA_ERR_INVALID_ARG, "context too long");
   return DBSA_OK;
-}
-
-float scale_log2(const dbsa_config *cfg) {
-  const double s = cfg->softmax_scale > 0.f ? (double)cfg->softmax_scale
-                                            : 1.0 / std::sqrt((double)cfg->head_dim);
-  return (float)(s * 1.4426950408889634);  // * log2(e)
-}
-
-int num_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    return 148;
-  return n;
 }
 
 // -------------------------------------------------------------- Stage-1 plan
@@ -798,15 +812,6 @@ BKLayout bk_layout(const dbsa_config *cfg, const int32_t *offs, int32_t nb) {
   l.v_hat = cv.take(cfg->dtype == DBSA_F32 ? (size_t)cfg->n_kv_heads * T * cfg->head_dim * 2 : 0);
   l.total = cv.total();
   return l;
-}
-
-dbsa_status check_ws(void *ws, size_t ws_bytes, size_t need) {
-  if (ws == nullptr) return fail(DBSA_ERR_WORKSPACE, "workspace is NULL");
-  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
-    return fail(DBSA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-  if (ws_bytes < need)
-    return fail(DBSA_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
-  return DBSA_OK;
 }
 
 template <typename T>

@@ -263,6 +263,23 @@ struct Stage2Args {
 // Sets the message dbsa_last_error() returns on this thread.
 void set_last_error(const char *msg);
 
+// What every entry point shares, for those outside dbsa_api.cu.
+dbsa_status fail(dbsa_status s, const char *fmt, ...);   // sets the message, returns s
+dbsa_status cuda_fail(cudaError_t e, const char *where);
+dbsa_status check_cfg(const dbsa_config *cfg);
+dbsa_status check_ws(void *ws, size_t ws_bytes, size_t need);
+float scale_log2(const dbsa_config *cfg);
+int num_sms();
+void count_launches(int n);
+uint64_t take_wait_expiry();   // the limit dbsa_test_wait_expiry() set, cleared
+// Records the profiling events (if any) around the main kernel of a call.
+struct ProfileScope {
+  cudaStream_t st;
+  cudaEvent_t stop;
+  explicit ProfileScope(cudaStream_t s);
+  ~ProfileScope();
+};
+
 // Scratch owned by the library rather than the caller: `bytes` of device
 // memory whose address (on the current device) resolve() returns.
 struct FixedScratch {

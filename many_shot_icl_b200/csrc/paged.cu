@@ -1,0 +1,576 @@
+// Paged cache: the append kernel, the attention call's preparation and merge
+// kernels, and the C entry points.
+//
+// The cache holds keys already rotated at their positions (the Stage-1 cache
+// holds them unrotated): a token's position in the shared prefix or behind it
+// never changes, so its key is rotated once, when it is appended, and every
+// later attention call streams it as it is.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "dbsa_internal.h"
+#include "paged.h"
+#include "paged_attn.h"
+#include "vec8.cuh"
+
+namespace dbsa {
+namespace {
+
+// 8 consecutive elements from fp32 registers, rounded to nearest even once.
+__device__ __forceinline__ void store8(bf16 *p, const float (&f)[8]) { store8_bf16(p, f); }
+__device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
+  reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+  reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+// ------------------------------------------------------------------- append
+// k'[i] = k[i] cos(pos w_i) - k[i + D/2] sin(pos w_i), k'[i + D/2] = k[i +
+// D/2] cos + k[i] sin; v is copied.  Every element is read and written once:
+// the kernel is bound by memory (long appends) or by the latency of its chain
+// row -> sequence -> page -> store (decode steps).  A block takes 256 / (D/16)
+// rows of one KV head; a thread 8 rotation pairs of the row's key and the
+// matching 16 elements of its value.
+template <typename T>
+struct AppendArgs {
+  const T *k, *v;
+  int64_t k_row, k_head, v_row, v_head;
+  PagedPool pool;
+  PagedBatch batch;
+  int64_t pos0;
+  RopeTables rope;
+};
+
+template <int D, typename T>
+__global__ void __launch_bounds__(256) append_kernel(const AppendArgs<T> a) {
+  pdl_enter();
+  constexpr int H = D / 2, CP = H / 8;
+  const int c = blockIdx.x % a.pool.Hkv;
+  const int row = (blockIdx.x / a.pool.Hkv) * (256 / CP) + threadIdx.x / CP;
+  const int i0 = (threadIdx.x % CP) * 8;
+  if (row >= a.batch.n_rows) return;
+  const T *ks = a.k + row * a.k_row + c * a.k_head, *vs = a.v + row * a.v_row + c * a.v_head;
+  const int2 st = row_token(a.batch, row);
+  if (st.x < 0 || st.y < 0) return;
+  const int page = __ldg(a.batch.page_table + (int64_t)st.x * a.batch.table_stride +
+                         (st.y >> a.pool.page_shift));
+  if (page < 0 || page >= a.pool.n_pages) return;
+  const int64_t dst =
+      page * a.pool.page_stride +
+      ((int64_t)c * a.pool.page_size + (st.y & (a.pool.page_size - 1))) * D + i0;
+  float lo[8], hi[8], cs[8], sn[8];
+  load8(ks + i0, lo);
+  load8(ks + H + i0, hi);
+  rope_cs8(a.rope, a.pos0 + st.y, i0, H, cs, sn);
+  rotate8(lo, hi, cs, sn);
+  T *kd = static_cast<T *>(a.pool.k) + dst, *vd = static_cast<T *>(a.pool.v) + dst;
+  store8(kd, lo);
+  store8(kd + H, hi);
+  copy8(vs + i0, vd);
+  copy8(vs + H + i0, vd + H);
+}
+
+// ------------------------------------------------------------ attention: plan
+// Exclusive prefix sum over the block's 256 threads; *total gets the sum.
+__device__ int64_t block_scan(int64_t x, int64_t *total) {
+  __shared__ int64_t warp_sum[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t inc = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(~0u, inc, d);
+    if (lane >= d) inc += y;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    if (w < warp) before += warp_sum[w];
+    all += warp_sum[w];
+  }
+  __syncthreads();
+  *total = all;
+  return before + inc - x;
+}
+
+// The own-token entries and their units, by one block.
+__device__ void build_plan(const AttendPlan &p, const PagedBatch &b) {
+  int64_t at = 0, total;
+  for (int s0 = 0; s0 < b.n_seqs; s0 += 256) {
+    const int s = s0 + threadIdx.x;
+    int64_t n = 0;
+    if (s < b.n_seqs) n = ((int64_t)seq_rows(b, s).n * p.g + p.tile_rows - 1) / p.tile_rows;
+    const int64_t first = at + block_scan(n, &total);
+    // more entries than max_entries need a decreasing row_ptr; none is written
+    if (s < b.n_seqs) p.first_entry[s] = (int32_t)min(first, (int64_t)p.max_entries);
+    at += total;
+  }
+  const int32_t ne = (int32_t)min(at, (int64_t)p.max_entries);
+  if (threadIdx.x == 0) {
+    p.first_entry[b.n_seqs] = ne;
+    *p.n_entries = ne;
+  }
+  __syncthreads();
+  int64_t units = 0;
+  for (int e0 = 0; e0 < ne; e0 += 256) {
+    const int e = e0 + threadIdx.x;
+    int64_t n = 0;
+    if (e < ne) {
+      int lo = 0, hi = b.n_seqs;   // the first sequence whose entries end past e
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (p.first_entry[mid + 1] > e) hi = mid; else lo = mid + 1;
+      }
+      const int rt = e - p.first_entry[lo];
+      p.entry[e] = make_int2(lo, rt);
+      const SeqRows s = seq_rows(b, lo);
+      // keys the last row of the tile sees
+      const int64_t end = min((int64_t)(rt + 1) * p.tile_rows, (int64_t)s.n * p.g) - 1;
+      const int64_t seen = min((int64_t)s.len, s.len - s.n + 1 + end / p.g);
+      n = seen > 0 ? (seen + p.tile_keys - 1) / p.tile_keys * p.Hkv : 0;
+    }
+    const int64_t first = units + block_scan(n, &total);
+    if (e < ne) p.units[e] = first;
+    units += total;
+  }
+  if (threadIdx.x == 0) p.units[ne] = units;
+}
+
+// Queries rotated at their positions and packed per KV head (one rounding to
+// the cache's type), the row table, the status word and (last block) the plan.
+template <int D, typename T>
+__global__ void __launch_bounds__(256) attend_prep_kernel(const AttendArgs a) {
+  pdl_enter();
+  constexpr int H = D / 2, CP = H / 8;
+  const AttendPlan &p = a.plan;
+  if (blockIdx.x == gridDim.x - 1) {
+    if (threadIdx.x < kStatusBytes / 4) a.status[threadIdx.x] = 0;
+    build_plan(p, a.batch);
+    return;
+  }
+  const int c = blockIdx.x % p.Hkv;
+  const int row = (blockIdx.x / p.Hkv) * (256 / CP) + threadIdx.x / CP;
+  const int cp = threadIdx.x % CP, i0 = cp * 8;
+  if (row >= a.batch.n_rows) return;
+  const int2 st = row_token(a.batch, row);
+  if (c == 0 && cp == 0) p.row_info[row] = st;
+  const bool live = st.x >= 0 && st.y >= 0;   // other rows: finite, never used
+  float cs[8], sn[8];
+  rope_cs8(a.rope, live ? (int64_t)p.prefix_len + st.y : 0, i0, H, cs, sn);
+  const T *src = static_cast<const T *>(a.q) + row * a.q_row_stride + (int64_t)c * p.g * D;
+  T *dst = static_cast<T *>(p.q_rot) + ((int64_t)c * p.rows + (int64_t)row * p.g) * D;
+#pragma unroll 4
+  for (int hl = 0; hl < p.g; ++hl) {
+    float lo[8], hi[8];
+    load8(src + (int64_t)hl * D + i0, lo);
+    load8(src + (int64_t)hl * D + H + i0, hi);
+    rotate8(lo, hi, cs, sn);
+    if (!live) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) lo[e] = hi[e] = 0.f;
+    }
+    store8(dst + (int64_t)hl * D + i0, lo);
+    store8(dst + (int64_t)hl * D + H + i0, hi);
+  }
+}
+
+// ----------------------------------------------------------- attention: merge
+// out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i over the row's pieces,
+// M = max m_i, in fp32.  One block of kMergeWarps warps per (row, head): each
+// warp takes every kMergeWarps-th piece, lanes the columns; the warps' sums
+// meet in shared memory.  Bound by the latency of reading the partials (L2).
+constexpr int kMergeWarps = 4;
+
+template <int D, typename T>
+__global__ void __launch_bounds__(32 * kMergeWarps) attend_merge_kernel(const AttendArgs a) {
+  pdl_enter();
+  constexpr int V = D / 32;   // columns per lane
+  const AttendPlan &p = a.plan;
+  const int Hq = p.Hkv * p.g;
+  const int row = blockIdx.x / Hq, h = blockIdx.x % Hq, c = h / p.g, hl = h % p.g;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int2 st = p.row_info[row];
+  if (st.x < 0) return;                      // a row of no sequence: left as it was
+  const int64_t pr = (int64_t)row * p.g + hl;
+  // partial rows first + i * step: n1 of the prefix, n2 of the own tokens
+  int64_t f1 = 0, f2 = 0;
+  int n1 = 0, n2 = 0;
+  if (st.y >= 0) {
+    if (p.n_groups > 0) {
+      const int64_t total = (int64_t)p.Hkv * p.prefix_tiles, u0 = (int64_t)c * p.prefix_tiles;
+      const int64_t j0 = part_of(u0, p.n_groups, total);
+      n1 = (int)(part_of(u0 + p.prefix_tiles - 1, p.n_groups, total) - j0) + 1;
+      f1 = (c + j0) * p.rows + pr;
+    }
+    const int32_t s0 = __ldg(a.batch.row_ptr + st.x);
+    const int64_t local = (int64_t)(row - s0) * p.g + hl;
+    const int32_t rt = (int32_t)(local / p.tile_rows);
+    const int64_t e = (int64_t)p.first_entry[st.x] + rt;
+    if (e < *p.n_entries) {
+      const int64_t total = p.units[*p.n_entries], u0 = p.units[e];
+      const int64_t tiles = (p.units[e + 1] - u0) / p.Hkv;
+      if (tiles > 0) {
+        const int64_t parts = own_parts(p, total);
+        const int64_t i0 = part_of(u0 + c * tiles, parts, total);
+        n2 = (int)(part_of(u0 + (c + 1) * tiles - 1, parts, total) - i0) + 1;
+        const SeqRows s = seq_rows(a.batch, st.x);
+        const int64_t tile0 = (int64_t)rt * p.tile_rows;
+        const int64_t n_rows = min((int64_t)p.tile_rows, (int64_t)s.n * p.g - tile0);
+        f2 = p.own_base + p.Hkv * ((int64_t)s0 * p.g + tile0) + c * n_rows + p.tile_rows * i0 +
+             (local - tile0);
+      }
+    }
+  }
+  const int n = n1 + n2;
+  auto at = [&](int i) { return i < n1 ? f1 + (int64_t)i * p.rows
+                                       : f2 + (int64_t)(i - n1) * p.tile_rows; };
+  // M over all pieces (every warp on its own)
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, p.ml[at(i)].x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
+  const float mu = M == -INFINITY ? 0.f : M;
+  float acc[V] = {}, L = 0.f;
+#pragma unroll 4
+  for (int i = warp; i < n; i += kMergeWarps) {
+    const int64_t r = at(i);
+    const float2 ml = p.ml[r];
+    const float w = exp2f(ml.x - mu);
+    L += w * ml.y;
+    const float *src = p.acc + r * D + lane * V;
+    if constexpr (V == 4) {
+      const float4 x = *reinterpret_cast<const float4 *>(src);
+      acc[0] += w * x.x;
+      acc[1] += w * x.y;
+      acc[2] += w * x.z;
+      acc[3] += w * x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2 *>(src);
+      acc[0] += w * x.x;
+      acc[1] += w * x.y;
+    }
+  }
+  __shared__ float sh[kMergeWarps][D + 1];
+#pragma unroll
+  for (int e = 0; e < V; ++e) sh[warp][lane * V + e] = acc[e];
+  if (lane == 0) sh[warp][D] = L;
+  __syncthreads();
+  for (int d = threadIdx.x; d < D; d += 32 * kMergeWarps) {
+    float num = 0.f, den = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+      num += sh[w][d];
+      den += sh[w][D];
+    }
+    from_f32(den > 0.f ? num / den : 0.f,
+             static_cast<T *>(a.out)[((int64_t)row * Hq + h) * D + d]);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Positions [0, n) a table buffer of that many bytes covers.
+int64_t table_positions(const dbsa_config *cfg, size_t bytes) {
+  const int64_t n_hi =
+      (int64_t)(bytes / (sizeof(float) * (size_t)cfg->head_dim)) - kRopeLo;
+  return n_hi > 0 ? n_hi * kRopeLo : 0;
+}
+
+dbsa_status check_paged(const dbsa_config *cfg, const dbsa_paged_cache *cache,
+                        const dbsa_paged_batch *b, int64_t pos0, const void *tables,
+                        size_t tables_bytes, PagedPool *pool, PagedBatch *batch,
+                        RopeTables *rope) {
+  dbsa_status s = check_cfg(cfg);
+  if (s != DBSA_OK) return s;
+  if (!cache || !b) return fail(DBSA_ERR_INVALID_ARG, "cache or batch is NULL");
+  if (!cache->k_pages || !cache->v_pages || !b->row_ptr || !b->seq_lens || !b->page_table ||
+      !tables)
+    return fail(DBSA_ERR_INVALID_ARG, "a tensor pointer is NULL");
+  if (!aligned16(cache->k_pages) || !aligned16(cache->v_pages) || !aligned16(tables))
+    return fail(DBSA_ERR_INVALID_ARG, "pages and tables must be 16-byte aligned");
+  if (((reinterpret_cast<uintptr_t>(b->row_ptr) | reinterpret_cast<uintptr_t>(b->seq_lens) |
+        reinterpret_cast<uintptr_t>(b->page_table)) & 3u) != 0)
+    return fail(DBSA_ERR_INVALID_ARG, "row_ptr, seq_lens and page_table must be 4-byte aligned");
+  const int ps = cache->page_size;
+  if (ps != 16 && ps != 32 && ps != 64 && ps != 128 && ps != 256)
+    return fail(DBSA_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256 (got %d)", ps);
+  if (cache->n_pages < 1) return fail(DBSA_ERR_INVALID_ARG, "n_pages must be >= 1");
+  const int64_t page = (int64_t)cfg->n_kv_heads * ps * cfg->head_dim;
+  if (cache->page_stride < page || cache->page_stride % 8 != 0)
+    return fail(DBSA_ERR_INVALID_ARG,
+                "page_stride must be a multiple of 8 and at least %lld (got %lld)",
+                (long long)page, (long long)cache->page_stride);
+  if (cache->page_stride > (int64_t(1) << 36))
+    return fail(DBSA_ERR_INVALID_ARG, "page_stride too large");
+  if (b->n_seqs < 1 || b->n_seqs > 65535)
+    return fail(DBSA_ERR_INVALID_ARG, "n_seqs must be 1..65535 (got %d)", b->n_seqs);
+  if (b->n_rows < 1) return fail(DBSA_ERR_INVALID_ARG, "n_rows must be >= 1");
+  if (b->table_width < 1 || b->table_stride < b->table_width)
+    return fail(DBSA_ERR_INVALID_ARG, "need 1 <= table_width <= table_stride");
+  const int64_t own_cap = (int64_t)b->table_width * ps;
+  if (pos0 < 0 || pos0 > (1 << 30) || own_cap > (1 << 30))
+    return fail(DBSA_ERR_INVALID_ARG, "sequences too long");
+  if (table_positions(cfg, tables_bytes) < pos0 + own_cap)
+    return fail(DBSA_ERR_INVALID_ARG, "tables cover %lld positions, the batch can reach %lld",
+                (long long)table_positions(cfg, tables_bytes), (long long)(pos0 + own_cap));
+  pool->k = cache->k_pages;
+  pool->v = cache->v_pages;
+  pool->page_stride = cache->page_stride;
+  pool->n_pages = cache->n_pages;
+  pool->page_size = ps;
+  pool->page_shift = ps == 16 ? 4 : ps == 32 ? 5 : ps == 64 ? 6 : ps == 128 ? 7 : 8;
+  pool->Hkv = cfg->n_kv_heads;
+  batch->row_ptr = b->row_ptr;
+  batch->seq_lens = b->seq_lens;
+  batch->page_table = b->page_table;
+  batch->n_seqs = b->n_seqs;
+  batch->n_rows = b->n_rows;
+  batch->table_width = b->table_width;
+  batch->table_stride = b->table_stride;
+  batch->cap = (int32_t)own_cap;
+  const int64_t n_hi = table_positions(cfg, tables_bytes) / kRopeLo;
+  *rope = rope_tables_at(static_cast<const float *>(tables), (int32_t)n_hi, cfg->head_dim);
+  return DBSA_OK;
+}
+
+// Cuts the prefix into ranges.  With n_row_tiles row tiles, w waves of the
+// CTAs hold w * n_ctas / n_row_tiles ranges; the smallest w (fewest partials)
+// that leaves under 5 % of the CTAs' time idle is taken, or the best of 8.
+int prefix_groups(int n_row_tiles, int n_ctas, int64_t units) {
+  int best = 1;
+  double best_use = 0;
+  for (int w = 1; w <= 8; ++w) {
+    const int64_t groups =
+        std::min<int64_t>(std::max<int64_t>((int64_t)w * n_ctas / n_row_tiles, 1), units);
+    const int64_t items = groups * n_row_tiles;
+    const double use = (double)items / (double)((items + n_ctas - 1) / n_ctas * n_ctas);
+    if (use > best_use + 1e-9) {
+      best = (int)groups;
+      best_use = use;
+    }
+    if (best_use > 0.95 || groups == units) break;
+  }
+  return best;
+}
+
+struct AttendLayout {
+  AttendPlan p;
+  size_t row_info, first_entry, entry, units, n_entries, q_rot, acc, ml, total;
+};
+AttendLayout attend_layout(const dbsa_config *cfg, int32_t n_seqs, int32_t n_rows,
+                           int64_t prefix_len) {
+  const AttendShape shape = attend_shape(cfg);
+  AttendLayout l{};
+  AttendPlan &p = l.p;
+  p.g = cfg->n_q_heads / cfg->n_kv_heads;
+  p.Hkv = cfg->n_kv_heads;
+  p.D = cfg->head_dim;
+  p.tile_rows = shape.tile_rows;
+  p.tile_keys = shape.tile_keys;
+  p.n_ctas = shape.n_ctas;
+  p.rows = n_rows * p.g;
+  p.n_row_tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
+  p.prefix_len = (int32_t)prefix_len;
+  p.prefix_tiles = (int32_t)((prefix_len + p.tile_keys - 1) / p.tile_keys);
+  p.n_groups = prefix_len == 0 ? 0
+                               : prefix_groups(p.n_row_tiles, p.n_ctas,
+                                               (int64_t)p.Hkv * p.prefix_tiles);
+  p.max_entries = n_seqs + p.rows / p.tile_rows;
+  p.own_base = prefix_len == 0 ? 0 : (int64_t)(p.Hkv + p.n_groups) * p.rows;
+  p.partial_rows = p.own_base + (int64_t)p.Hkv * p.rows + (int64_t)p.tile_rows * p.n_ctas;
+  const size_t elt = cfg->dtype == DBSA_F32 ? 4 : 2;
+  size_t off = kStatusBytes;
+  auto take = [&](size_t bytes) {
+    const size_t o = align_up(off);
+    off = o + bytes;
+    return o;
+  };
+  l.row_info = take((size_t)n_rows * sizeof(int2));
+  l.first_entry = take(((size_t)n_seqs + 1) * sizeof(int32_t));
+  l.entry = take((size_t)p.max_entries * sizeof(int2));
+  l.units = take(((size_t)p.max_entries + 1) * sizeof(int64_t));
+  l.n_entries = take(sizeof(int32_t));
+  l.q_rot = take((size_t)p.Hkv * p.rows * p.D * elt);
+  l.acc = take((size_t)p.partial_rows * p.D * sizeof(float));
+  l.ml = take((size_t)p.partial_rows * sizeof(float2));
+  l.total = align_up(off);
+  return l;
+}
+
+// n_rows * g and the partial rows stay far inside 32 and 64 bits.
+dbsa_status check_attend_size(const dbsa_config *cfg, int32_t n_seqs, int32_t n_rows,
+                              int64_t prefix_len) {
+  if (n_seqs < 1 || n_seqs > 65535)
+    return fail(DBSA_ERR_INVALID_ARG, "n_seqs must be 1..65535 (got %d)", n_seqs);
+  if (n_rows < 1 || (int64_t)n_rows * cfg->n_q_heads > (1 << 28))
+    return fail(DBSA_ERR_INVALID_ARG, "n_rows must be 1..%d (got %d)",
+                (1 << 28) / cfg->n_q_heads, n_rows);
+  if (prefix_len < 0 || prefix_len > (1 << 30))
+    return fail(DBSA_ERR_INVALID_ARG, "prefix_len must be 0..2^30");
+  return DBSA_OK;
+}
+
+template <int D, typename T>
+cudaError_t launch_attend_t(const AttendArgs &a, cudaStream_t st) {
+  constexpr int RPB = 256 / (D / 16);
+  const int64_t blocks = (int64_t)((a.batch.n_rows + RPB - 1) / RPB) * a.plan.Hkv + 1;
+  cudaError_t e = pdl_launch(attend_prep_kernel<D, T>, dim3((unsigned)blocks), dim3(256), 0, st, a);
+  if (e != cudaSuccess) return e;
+  {
+    ProfileScope prof(st);
+    e = launch_attend_pieces(a, D, sizeof(T) == 4, st);
+  }
+  if (e != cudaSuccess) return e;
+  return pdl_launch(attend_merge_kernel<D, T>,
+                    dim3((unsigned)a.batch.n_rows * a.plan.Hkv * a.plan.g), dim3(32 * kMergeWarps),
+                    0, st, a);
+}
+
+template <int D, typename T>
+cudaError_t launch_append_t(const void *k, const void *v, const int64_t (&str)[4],
+                            const PagedPool &pool, const PagedBatch &batch, int64_t pos0,
+                            const RopeTables &rope, cudaStream_t st) {
+  constexpr int RPB = 256 / (D / 16);
+  AppendArgs<T> a;
+  a.k = static_cast<const T *>(k);
+  a.v = static_cast<const T *>(v);
+  a.k_row = str[0];
+  a.k_head = str[1];
+  a.v_row = str[2];
+  a.v_head = str[3];
+  a.pool = pool;
+  a.batch = batch;
+  a.pos0 = pos0;
+  a.rope = rope;
+  const int64_t blocks = (int64_t)((batch.n_rows + RPB - 1) / RPB) * pool.Hkv;
+  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  return pdl_launch(append_kernel<D, T>, dim3((unsigned)blocks), dim3(256), 0, st, a);
+}
+
+}  // namespace
+}  // namespace dbsa
+
+using namespace dbsa;
+
+extern "C" {
+
+size_t dbsa_rope_tables_size(const dbsa_config *cfg, int64_t n_pos) {
+  if (check_cfg(cfg) != DBSA_OK) return 0;
+  if (n_pos < 1 || n_pos > (int64_t(1) << 31)) {
+    fail(DBSA_ERR_INVALID_ARG, "n_pos must be 1..2^31");
+    return 0;
+  }
+  return rope_table_bytes((int32_t)((n_pos + kRopeLo - 1) / kRopeLo), cfg->head_dim);
+}
+
+dbsa_status dbsa_rope_tables(const dbsa_config *cfg, int64_t n_pos, void *tables,
+                             size_t tables_bytes, void *stream) {
+  const size_t need = dbsa_rope_tables_size(cfg, n_pos);
+  if (need == 0) return check_cfg(cfg) != DBSA_OK ? check_cfg(cfg) : DBSA_ERR_INVALID_ARG;
+  if (!tables || !aligned16(tables))
+    return fail(DBSA_ERR_INVALID_ARG, "tables is NULL or not 16-byte aligned");
+  if (tables_bytes < need)
+    return fail(DBSA_ERR_INVALID_ARG, "tables too small: %zu < %zu bytes", tables_bytes, need);
+  // every position the buffer has room for, so that its size alone says which
+  // positions it covers
+  const int32_t n_hi = (int32_t)(table_positions(cfg, tables_bytes) / kRopeLo);
+  const cudaError_t e = launch_rope_tables(static_cast<float *>(tables), n_hi, cfg->head_dim,
+                                           cfg->rope_theta, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rope tables");
+  count_launches(1);
+  return DBSA_OK;
+}
+
+dbsa_status dbsa_paged_append(const dbsa_config *cfg, const void *k, int64_t k_row_stride,
+                              int64_t k_head_stride, const void *v, int64_t v_row_stride,
+                              int64_t v_head_stride, const dbsa_paged_cache *cache,
+                              const dbsa_paged_batch *batch, int64_t pos0, const void *tables,
+                              size_t tables_bytes, void *stream) {
+  PagedPool pool;
+  PagedBatch b;
+  RopeTables rope;
+  const dbsa_status s =
+      check_paged(cfg, cache, batch, pos0, tables, tables_bytes, &pool, &b, &rope);
+  if (s != DBSA_OK) return s;
+  if (!k || !v) return fail(DBSA_ERR_INVALID_ARG, "a tensor pointer is NULL");
+  if (!aligned16(k) || !aligned16(v))
+    return fail(DBSA_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
+  const int64_t str[4] = {k_row_stride, k_head_stride, v_row_stride, v_head_stride};
+  for (int64_t x : str)
+    if (x % 8 != 0) return fail(DBSA_ERR_INVALID_ARG, "strides must be multiples of 8");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool f32 = cfg->dtype == DBSA_F32;
+  cudaError_t e;
+  if (cfg->head_dim == 128)
+    e = f32 ? launch_append_t<128, float>(k, v, str, pool, b, pos0, rope, st)
+            : launch_append_t<128, bf16>(k, v, str, pool, b, pos0, rope, st);
+  else
+    e = f32 ? launch_append_t<64, float>(k, v, str, pool, b, pos0, rope, st)
+            : launch_append_t<64, bf16>(k, v, str, pool, b, pos0, rope, st);
+  if (e != cudaSuccess) return cuda_fail(e, "paged append");
+  count_launches(1);
+  return DBSA_OK;
+}
+
+size_t dbsa_shared_prefix_workspace_size(const dbsa_config *cfg, int32_t n_seqs, int32_t n_rows,
+                                         int64_t prefix_len) {
+  if (check_cfg(cfg) != DBSA_OK || check_attend_size(cfg, n_seqs, n_rows, prefix_len) != DBSA_OK)
+    return 0;
+  return attend_layout(cfg, n_seqs, n_rows, prefix_len).total;
+}
+
+dbsa_status dbsa_shared_prefix_attend(const dbsa_config *cfg, const void *q,
+                                      int64_t q_row_stride, const dbsa_paged_cache *cache,
+                                      const int32_t *prefix_pages, int64_t prefix_len,
+                                      const dbsa_paged_batch *batch, const void *tables,
+                                      size_t tables_bytes, void *out, void *workspace,
+                                      size_t ws_bytes, void *stream) {
+  const uint64_t wait_expiry = take_wait_expiry();
+  AttendArgs a{};
+  dbsa_status s = check_paged(cfg, cache, batch, prefix_len, tables, tables_bytes, &a.pool,
+                              &a.batch, &a.rope);
+  if (s != DBSA_OK) return s;
+  if ((s = check_attend_size(cfg, batch->n_seqs, batch->n_rows, prefix_len)) != DBSA_OK) return s;
+  if (!q || !out || (prefix_len > 0 && !prefix_pages))
+    return fail(DBSA_ERR_INVALID_ARG, "a tensor pointer is NULL");
+  if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(prefix_pages) & 3u) != 0)
+    return fail(DBSA_ERR_INVALID_ARG, "q and out must be 16-byte aligned, prefix_pages 4-byte");
+  if (q_row_stride % 8 != 0)
+    return fail(DBSA_ERR_INVALID_ARG, "q_row_stride must be a multiple of 8");
+  const AttendLayout l = attend_layout(cfg, batch->n_seqs, batch->n_rows, prefix_len);
+  if ((s = check_ws(workspace, ws_bytes, l.total)) != DBSA_OK) return s;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  a.plan = l.p;
+  a.plan.row_info = reinterpret_cast<int2 *>(ws + l.row_info);
+  a.plan.first_entry = reinterpret_cast<int32_t *>(ws + l.first_entry);
+  a.plan.entry = reinterpret_cast<int2 *>(ws + l.entry);
+  a.plan.units = reinterpret_cast<int64_t *>(ws + l.units);
+  a.plan.n_entries = reinterpret_cast<int32_t *>(ws + l.n_entries);
+  a.plan.q_rot = ws + l.q_rot;
+  a.plan.acc = reinterpret_cast<float *>(ws + l.acc);
+  a.plan.ml = reinterpret_cast<float2 *>(ws + l.ml);
+  a.prefix_pages = prefix_pages;
+  a.q = q;
+  a.q_row_stride = q_row_stride;
+  a.out = out;
+  a.scale_log2 = scale_log2(cfg);
+  a.status = reinterpret_cast<int *>(ws);
+  a.wait_limit_ns = wait_expiry;
+  a.withhold_tiles = wait_expiry != 0;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool f32 = cfg->dtype == DBSA_F32;
+  cudaError_t e;
+  if (cfg->head_dim == 128)
+    e = f32 ? launch_attend_t<128, float>(a, st) : launch_attend_t<128, bf16>(a, st);
+  else
+    e = f32 ? launch_attend_t<64, float>(a, st) : launch_attend_t<64, bf16>(a, st);
+  if (e != cudaSuccess) return cuda_fail(e, "shared-prefix attention");
+  count_launches(3);
+  return DBSA_OK;
+}
+
+}  // extern "C"

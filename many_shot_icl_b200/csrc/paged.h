@@ -1,0 +1,248 @@
+// Internal declarations of the paged cache and the shared-prefix attention:
+// the batch as the kernels see it, the device-built plan, and how the work is
+// cut into pieces.  Not part of the public ABI.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "dbsa_internal.h"
+
+namespace dbsa {
+
+struct PagedPool {
+  void *k, *v;
+  int64_t page_stride;    // elements
+  int32_t n_pages, page_size, page_shift;   // page_size = 1 << page_shift
+  int32_t Hkv;
+};
+
+struct PagedBatch {
+  const int32_t *row_ptr, *seq_lens, *page_table;
+  int32_t n_seqs, n_rows, table_width, table_stride;
+  int32_t cap;            // table_width * page_size
+};
+
+// The rows of one sequence in the batch and its own length with them; n = 0
+// when its row_ptr entries are not rows of the batch.
+struct SeqRows {
+  int32_t row0, n, len;
+};
+__device__ __forceinline__ SeqRows seq_rows(const PagedBatch &b, int s) {
+  SeqRows r;
+  r.row0 = __ldg(b.row_ptr + s);
+  const int32_t e = __ldg(b.row_ptr + s + 1);
+  r.n = (r.row0 >= 0 && e <= b.n_rows && e > r.row0) ? e - r.row0 : 0;
+  r.len = __ldg(b.seq_lens + s);
+  if (r.len < 0 || r.len > b.cap) r.len = 0;
+  return r;
+}
+
+// (sequence, own token) of a row: sequence -1 for a row of none, a negative
+// token for padding.  A decode step has one row per sequence in order, so row
+// r is tried as sequence r before the search.
+__device__ __forceinline__ int2 row_token(const PagedBatch &b, int row) {
+  int s = min(row, b.n_seqs - 1);
+  if (!(__ldg(b.row_ptr + s) <= row && row < __ldg(b.row_ptr + s + 1))) {
+    int lo = 0, hi = b.n_seqs;   // the first sequence that ends past the row
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(b.row_ptr + mid + 1) > row) hi = mid; else lo = mid + 1;
+    }
+    if (lo == b.n_seqs) return make_int2(-1, 0);
+    s = lo;
+  }
+  const SeqRows r = seq_rows(b, s);
+  if (row < r.row0 || row >= r.row0 + r.n) return make_int2(-1, 0);
+  return make_int2(s, r.len - r.n + (row - r.row0));
+}
+
+// ---- the plan of one attention call ----
+//
+// Query rows are packed per KV head: packed row r * g + hl is the batch's row
+// r, local head hl.  The prefix is attended to by tiles of tile_rows packed
+// rows, whichever sequences they belong to; own tokens by tiles that do not
+// straddle a sequence.  Keys are counted in tiles of tile_keys.
+//
+// Prefix: the Hkv * prefix_tiles (KV head, key tile) units are cut into
+// n_groups equal ranges, and each (range, row tile) is one item; the n_row_tiles
+// items of a range are next to each other, so that they run at the same time
+// and read its keys from memory once.  Item i goes to CTA i % n_ctas.
+// Own tokens: the units of all (sequence, row tile, KV head) entries, in that
+// order, are cut into n_ctas equal ranges (or one per unit, if those are fewer),
+// one per CTA.
+//
+// Every (item or range, KV head, row tile) intersection is a piece: it leaves
+// one partial (row maximum, sum of exponentials, weighted values) per row.
+// Piece (head c, range j) of the prefix keeps packed row p at partial row
+// (c + j) * rows + p: c + j is unique along the ranges, because from one piece
+// to the next either the head or the range moves on.  The piece of own-token
+// entry e in CTA i starts at own_base + first(e) + tile_rows * i, where
+// first(e) counts the rows of the entries before it: again unique, since a next
+// piece adds either the rows of e or tile_rows.
+struct AttendPlan {
+  int32_t g, Hkv, D;
+  int32_t tile_rows, tile_keys;
+  int32_t rows;            // packed rows per KV head: n_rows * g
+  int32_t n_row_tiles;     // ceil(rows / tile_rows)
+  int32_t prefix_len, prefix_tiles;
+  int32_t n_groups;        // ranges of the prefix
+  int32_t n_ctas;
+  int32_t max_entries;     // own-token (sequence, row tile) entries, at most
+  int64_t own_base;        // first own-token partial row
+  int64_t partial_rows;
+  // device
+  int2 *row_info;          // [n_rows]: row_token()
+  int32_t *first_entry;    // [n_seqs + 1]
+  int2 *entry;             // [max_entries]: (sequence, row tile)
+  int64_t *units;          // [max_entries + 1]: key-tile units (all heads) before entry e
+  int32_t *n_entries;
+  void *q_rot;             // [Hkv][rows][D], cfg->dtype, rotated
+  float *acc;              // [partial_rows][D], not normalised
+  float2 *ml;              // [partial_rows]: (maximum in log2 units, sum)
+};
+
+// One piece: rows of a tile against key tiles [kt0, kt1) of one list of pages.
+struct Piece {
+  int32_t c;               // KV head
+  int32_t row0, n_rows;    // packed rows
+  int32_t kt0, kt1;
+  int32_t n_keys;          // keys of the list that exist
+  int32_t see0;            // row i sees keys below see0 + (off + i) / g, and n_keys
+  int32_t off;
+  int32_t shared;          // the prefix (1) or own tokens (0)
+  const int32_t *pages;
+  int64_t partial;         // partial row of the piece's first row
+};
+
+// The smallest j with floor((j + 1) * total / parts) > x, i.e. the part of
+// [0, total) cut into `parts` ranges that holds x.
+__host__ __device__ __forceinline__ int64_t part_of(int64_t x, int64_t parts, int64_t total) {
+  return ((x + 1) * parts - 1) / total;
+}
+
+// CTAs that share the own-token units: no range may be empty, because the
+// merge reads a partial of every CTA from a row's first to its last.
+__device__ __forceinline__ int64_t own_parts(const AttendPlan &p, int64_t units) {
+  return min((int64_t)p.n_ctas, units);
+}
+
+// Walks the pieces of one CTA in order.
+struct PieceWalk {
+  // prefix
+  int64_t item;            // next (range, row tile) item
+  int64_t pu, pend;        // units of the current item still to emit
+  int32_t pj, prt;
+  // own tokens
+  int64_t u, uend;
+  int32_t e;
+  bool own;
+  int32_t cta;
+
+  __device__ __forceinline__ void init(int32_t cta_) {
+    cta = cta_;
+    item = cta_;
+    pu = pend = 0;
+    pj = prt = 0;
+    own = false;
+    u = uend = 0;
+    e = 0;
+  }
+
+  __device__ bool next(const AttendPlan &p, const PagedBatch &b, const int32_t *prefix_pages,
+                       Piece &o) {
+    if (!own) {
+      if (pu == pend) {
+        if (item < (int64_t)p.n_groups * p.n_row_tiles) {
+          pj = (int32_t)(item / p.n_row_tiles);
+          prt = (int32_t)(item % p.n_row_tiles);
+          const int64_t total = (int64_t)p.Hkv * p.prefix_tiles;
+          pu = pj * total / p.n_groups;
+          pend = (pj + 1) * total / p.n_groups;
+          item += p.n_ctas;
+        } else {
+          own = true;
+          const int32_t ne = *p.n_entries;
+          const int64_t total = p.units[ne];
+          const int64_t parts = own_parts(p, total);
+          if (cta < parts) {
+            u = cta * total / parts;
+            uend = (cta + 1) * total / parts;
+          }
+          int lo = 0, hi = ne;    // the first entry that ends past u
+          while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (p.units[mid + 1] > u) hi = mid; else lo = mid + 1;
+          }
+          e = lo;
+        }
+      }
+      if (!own) {
+        o.c = (int32_t)(pu / p.prefix_tiles);
+        o.kt0 = (int32_t)(pu % p.prefix_tiles);
+        const int64_t n = min((int64_t)(p.prefix_tiles - o.kt0), pend - pu);
+        o.kt1 = o.kt0 + (int32_t)n;
+        pu += n;
+        o.row0 = prt * p.tile_rows;
+        o.n_rows = min(p.tile_rows, p.rows - o.row0);
+        o.n_keys = p.prefix_len;
+        o.see0 = p.prefix_len;
+        o.off = 0;
+        o.shared = 1;
+        o.pages = prefix_pages;
+        o.partial = (int64_t)(o.c + pj) * p.rows + o.row0;
+        return true;
+      }
+    }
+    if (u >= uend) return false;
+    int64_t first = p.units[e], last = p.units[e + 1];
+    while (last <= u) {
+      ++e;
+      first = last;
+      last = p.units[e + 1];
+    }
+    const int2 en = p.entry[e];
+    const int32_t tiles = (int32_t)((last - first) / p.Hkv);
+    const int64_t rem = u - first;
+    o.c = (int32_t)(rem / tiles);
+    o.kt0 = (int32_t)(rem % tiles);
+    const int64_t n = min((int64_t)(tiles - o.kt0), uend - u);
+    o.kt1 = o.kt0 + (int32_t)n;
+    u += n;
+    const SeqRows s = seq_rows(b, en.x);
+    const int32_t packed = s.n * p.g;
+    o.off = en.y * p.tile_rows;
+    o.row0 = s.row0 * p.g + o.off;
+    o.n_rows = min(p.tile_rows, packed - o.off);
+    o.n_keys = s.len;
+    o.see0 = s.len - s.n + 1;
+    o.shared = 0;
+    o.pages = b.page_table + (int64_t)en.x * b.table_stride;
+    o.partial = p.own_base + (int64_t)p.Hkv * o.row0 + (int64_t)o.c * o.n_rows +
+                (int64_t)p.tile_rows * cta;
+    return true;
+  }
+};
+
+// Keys row i of a piece may see (it sees keys below the result).
+__device__ __forceinline__ int32_t keys_seen(const Piece &p, int g, int i) {
+  return p.shared ? p.n_keys : min(p.n_keys, p.see0 + (p.off + i) / g);
+}
+
+struct AttendArgs {
+  PagedPool pool;
+  PagedBatch batch;
+  AttendPlan plan;
+  const int32_t *prefix_pages;
+  const void *q;
+  int64_t q_row_stride;
+  void *out;
+  RopeTables rope;
+  float scale_log2;
+  int *status;
+  uint64_t wait_limit_ns;
+  int32_t withhold_tiles;
+};
+
+}  // namespace dbsa

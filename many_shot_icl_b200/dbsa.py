@@ -28,7 +28,8 @@ SYMBOLS = (
     "dbsa_stage1_tile_count", "dbsa_version", "dbsa_kernel_launches", "dbsa_set_profile_events",
     "dbsa_gather_rope_attend_noalloc", "dbsa_block_keys_size", "dbsa_block_keys",
     "dbsa_gather_rope_attend_prepared", "dbsa_noalloc_read_status", "dbsa_test_wait_expiry",
-    "dbsa_host_allocation_calls",
+    "dbsa_host_allocation_calls", "dbsa_rope_tables_size", "dbsa_rope_tables",
+    "dbsa_paged_append", "dbsa_shared_prefix_workspace_size", "dbsa_shared_prefix_attend",
 )
 
 
@@ -51,6 +52,19 @@ class TileItem(ctypes.Structure):
                 ("n_rows", ctypes.c_int32), ("n_ranges", ctypes.c_int32), ("block", ctypes.c_int32),
                 ("k_row0", ctypes.c_int32 * 2), ("v_row0", ctypes.c_int32 * 2),
                 ("pos0", ctypes.c_int32 * 2), ("len", ctypes.c_int32 * 2)]
+
+
+class PagedCache(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
+
+
+class PagedBatch(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_rows", ctypes.c_int32),
+                ("row_ptr", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("table_width", ctypes.c_int32),
+                ("table_stride", ctypes.c_int32)]
 
 
 @dataclass(frozen=True)
@@ -130,6 +144,19 @@ def load(path: str = LIB_PATH):
     lib.dbsa_test_wait_expiry.restype = None
     lib.dbsa_host_allocation_calls.argtypes = []
     lib.dbsa_host_allocation_calls.restype = i64
+    lib.dbsa_rope_tables_size.argtypes = [cfgp, i64]
+    lib.dbsa_rope_tables_size.restype = sz
+    lib.dbsa_rope_tables.argtypes = [cfgp, i64, vp, sz, vp]
+    lib.dbsa_rope_tables.restype = ctypes.c_int
+    cachep, batchp = ctypes.POINTER(PagedCache), ctypes.POINTER(PagedBatch)
+    lib.dbsa_paged_append.argtypes = [cfgp, vp, i64, i64, vp, i64, i64, cachep, batchp, i64, vp,
+                                      sz, vp]
+    lib.dbsa_paged_append.restype = ctypes.c_int
+    lib.dbsa_shared_prefix_workspace_size.argtypes = [cfgp, i32, i32, i64]
+    lib.dbsa_shared_prefix_workspace_size.restype = sz
+    lib.dbsa_shared_prefix_attend.argtypes = [cfgp, vp, i64, cachep, vp, i64, batchp, vp, sz, vp,
+                                              vp, sz, vp]
+    lib.dbsa_shared_prefix_attend.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -320,3 +347,156 @@ def selection_csr(selections) -> tuple[np.ndarray, np.ndarray]:
     ptr[1:] = np.cumsum([len(s) for s in selections])
     return ptr, (np.concatenate(selections).astype(np.int32) if selections else
                  np.zeros(0, np.int32))
+
+
+def _refuse(msg: str):
+    raise DbsaError(ERR_INVALID_ARG, msg)
+
+
+class _Call:
+    """Device and stream of a call on tensors of one device: that device is
+    made current for the call when it is not, and the stream defaults to its
+    current one."""
+
+    def __init__(self, device, stream):
+        import torch
+        self._guard = None
+        if device.index != torch.cuda.current_device():
+            self._guard = torch.cuda.device(device)
+        self._device, self._torch, self.stream = device, torch, stream
+
+    def __enter__(self) -> int:
+        if self._guard is not None:
+            self._guard.__enter__()
+        s = self._torch.cuda.current_stream(self._device) if self.stream is None else self.stream
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _on_device(device, **tensors):
+    for name, t in tensors.items():
+        if not t.is_cuda or t.device != device:
+            _refuse("%s must be on the CUDA device of the pages (%s)" % (name, device))
+
+
+def _strides(t):
+    """Row and head stride of [rows][heads][d]; 0 for a dimension of one."""
+    return tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in (0, 1))
+
+
+def _paged_args(cfg: DbsaConfig, k_pages, v_pages, page_table, row_ptr, seq_lens, tables, n_rows):
+    """The cache and batch structs of a call, after checking the tensors."""
+    import torch
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        _refuse("pages must be [n_pages][n_kv_heads][page_size][head_dim], keys and values alike")
+    n_pages, hkv, page_size, d = k_pages.shape
+    if hkv != cfg.n_kv_heads or d != cfg.head_dim:
+        _refuse("pages of %d heads of %d elements; cfg has %d of %d"
+                % (hkv, d, cfg.n_kv_heads, cfg.head_dim))
+    stride = k_pages.stride(0) if n_pages > 1 else hkv * page_size * d
+    dtype = torch.float32 if cfg.dtype == "f32" else torch.bfloat16
+    for t in (k_pages, v_pages):
+        st = t.stride()
+        if (t.dtype != dtype or st[3] != 1 or st[2] != d or (hkv > 1 and st[1] != page_size * d)
+                or (n_pages > 1 and st[0] != stride)):
+            _refuse("pages must be %s, contiguous inside a page, with one page stride" % dtype)
+    n_seqs = seq_lens.shape[0]
+    if (row_ptr.dtype != torch.int32 or seq_lens.dtype != torch.int32
+            or page_table.dtype != torch.int32 or seq_lens.dim() != 1
+            or row_ptr.shape != (n_seqs + 1,) or page_table.dim() != 2
+            or page_table.shape[0] != n_seqs):
+        _refuse("row_ptr [n_seqs + 1], seq_lens [n_seqs] and page_table [n_seqs][width] must be "
+                "int32")
+    width = page_table.shape[1]
+    if (not row_ptr.is_contiguous() or not seq_lens.is_contiguous()
+            or (width > 1 and page_table.stride(1) != 1)):
+        _refuse("row_ptr and seq_lens must be contiguous, and the rows of page_table")
+    if not tables.is_contiguous():
+        _refuse("tables must be contiguous")
+    _on_device(k_pages.device, k_pages=k_pages, v_pages=v_pages, page_table=page_table,
+               row_ptr=row_ptr, seq_lens=seq_lens, tables=tables)
+    cache = PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), stride, n_pages, page_size)
+    table_stride = page_table.stride(0) if n_seqs > 1 else max(width, 1)
+    batch = PagedBatch(n_seqs, n_rows, row_ptr.data_ptr(), seq_lens.data_ptr(),
+                       page_table.data_ptr(), width, table_stride)
+    return cache, batch, dtype
+
+
+def rope_tables_size(cfg: DbsaConfig, n_pos: int) -> int:
+    c = cfg.c()
+    return int(load().dbsa_rope_tables_size(ctypes.byref(c), n_pos))
+
+
+def rope_tables(cfg: DbsaConfig, n_pos: int, buf, stream=None):
+    """Angle tables for positions [0, n_pos) into buf (uint8 device tensor of
+    rope_tables_size() bytes), for paged_append and shared_prefix_attend."""
+    if not buf.is_cuda or not buf.is_contiguous():
+        _refuse("buf must be a contiguous CUDA tensor")
+    c = cfg.c()
+    with _Call(buf.device, stream) as st:
+        _check(load().dbsa_rope_tables(ctypes.byref(c), n_pos, _dp(buf),
+                                       buf.numel() * buf.element_size(), st))
+
+
+def paged_append(cfg: DbsaConfig, k, v, k_pages, v_pages, page_table, row_ptr, seq_lens, tables,
+                 pos0: int = 0, stream=None):
+    """Append the rows k, v [n_rows][n_kv_heads][head_dim] (any row and head
+    stride) of a batch to their sequences' pages, keys rotated at pos0 + their
+    index in the sequence (see dbsa_paged_append)."""
+    cache, batch, dtype = _paged_args(cfg, k_pages, v_pages, page_table, row_ptr, seq_lens, tables,
+                                      k.shape[0])
+    _on_device(k_pages.device, k=k, v=v)
+    shape = (k.shape[0], cfg.n_kv_heads, cfg.head_dim)
+    for t in (k, v):
+        if t.dtype != dtype or t.shape != shape or t.stride(2) != 1:
+            _refuse("k and v must be %s [n_rows][n_kv_heads][head_dim] with contiguous elements"
+                    % dtype)
+    c = cfg.c()
+    with _Call(k_pages.device, stream) as st:
+        _check(load().dbsa_paged_append(
+            ctypes.byref(c), _dp(k), *_strides(k), _dp(v), *_strides(v),
+            ctypes.byref(cache), ctypes.byref(batch), pos0, _dp(tables),
+            tables.numel() * tables.element_size(), st))
+
+
+def shared_prefix_workspace_size(cfg: DbsaConfig, n_seqs: int, n_rows: int,
+                                 prefix_len: int) -> int:
+    c = cfg.c()
+    return int(load().dbsa_shared_prefix_workspace_size(ctypes.byref(c), n_seqs, n_rows,
+                                                        prefix_len))
+
+
+def shared_prefix_attend(cfg: DbsaConfig, q, k_pages, v_pages, prefix_pages, prefix_len: int,
+                         page_table, row_ptr, seq_lens, tables, out, workspace, stream=None):
+    """Attention of the rows q [n_rows][n_q_heads][head_dim] (any row stride)
+    over a shared prefix and, causally, each row's own sequence, into out of
+    the same shape, contiguous (see dbsa_shared_prefix_attend).  prefix_pages
+    may be None when prefix_len is 0."""
+    import torch
+    cache, batch, dtype = _paged_args(cfg, k_pages, v_pages, page_table, row_ptr, seq_lens, tables,
+                                      q.shape[0])
+    _on_device(k_pages.device, q=q, out=out, workspace=workspace)
+    shape = (q.shape[0], cfg.n_q_heads, cfg.head_dim)
+    if (q.dtype != dtype or q.shape != shape or q.stride(2) != 1
+            or (cfg.n_q_heads > 1 and q.stride(1) != cfg.head_dim)):
+        _refuse("q must be %s [n_rows][n_q_heads][head_dim], each row contiguous" % dtype)
+    if out.dtype != dtype or out.shape != shape or not out.is_contiguous():
+        _refuse("out must be %s, contiguous, of q's shape" % dtype)
+    if not workspace.is_contiguous():
+        _refuse("workspace must be contiguous")
+    if prefix_len > 0:
+        if prefix_pages is None:
+            _refuse("prefix_pages is None")
+        _on_device(k_pages.device, prefix_pages=prefix_pages)
+        if (prefix_pages.dtype != torch.int32 or not prefix_pages.is_contiguous()
+                or prefix_pages.numel() * cache.page_size < prefix_len):
+            _refuse("prefix_pages must be contiguous int32, one entry per page of the prefix")
+    c = cfg.c()
+    with _Call(k_pages.device, stream) as st:
+        _check(load().dbsa_shared_prefix_attend(
+            ctypes.byref(c), _dp(q), _strides(q)[0], ctypes.byref(cache), _dp(prefix_pages),
+            prefix_len, ctypes.byref(batch), _dp(tables), tables.numel() * tables.element_size(),
+            _dp(out), _dp(workspace), workspace.numel() * workspace.element_size(), st))
