@@ -1,13 +1,16 @@
 // Shared-prefix attention, the pieces: per (row tile, KV head, run of key
 // tiles) one pass over the keys with the running maximum and sum of a softmax,
 // leaving a partial per row.
+#include <cuda.h>
 #include <cuda_bf16.h>
+#include <cudaTypedefs.h>
 
-#include <algorithm>
+#include <mutex>
 
 #include "dbsa_internal.h"
 #include "paged.h"
 #include "paged_attn.h"
+#include "sm100.cuh"
 #include "vec8.cuh"
 
 namespace dbsa {
@@ -36,13 +39,14 @@ __device__ __forceinline__ void load8_f32(const T *src, float *dst) {
   reinterpret_cast<float4 *>(dst)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(kSimpleThreads) attend_simple_kernel(const AttendArgs a) {
   pdl_enter();
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SimpleSmem<D> &sm = *reinterpret_cast<SimpleSmem<D> *>(smem_raw);
   constexpr int V = D / 32, CH = D / 8;
   const AttendPlan &p = a.plan;
+  using T = float;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   PieceWalk walk;
   walk.init(blockIdx.x);
@@ -157,27 +161,530 @@ __global__ void __launch_bounds__(kSimpleThreads) attend_simple_kernel(const Att
   }
 }
 
-template <int D, typename T>
+template <int D>
 cudaError_t launch_simple(const AttendArgs &a, cudaStream_t st) {
   const cudaError_t e =
-      cudaFuncSetAttribute(attend_simple_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      cudaFuncSetAttribute(attend_simple_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)sizeof(SimpleSmem<D>));
   if (e != cudaSuccess) return e;
-  return pdl_launch(attend_simple_kernel<D, T>, dim3(a.plan.n_ctas), dim3(kSimpleThreads),
+  return pdl_launch(attend_simple_kernel<D>, dim3(a.plan.n_ctas), dim3(kSimpleThreads),
                     sizeof(SimpleSmem<D>), st, a);
+}
+
+// ------------------------------------------------------ tensor-core kernel
+// bf16 caches: tiles of 128 packed rows against 128 keys on tcgen05.
+//
+// Two CTAs per SM, 192 threads each, half of the SM's shared memory and tensor
+// memory each: while one CTA's softmax runs, the tensor core works for the
+// other.  Per CTA:
+//   warp 4     walks the pieces, publishes each in a ring of kPieceSlots, and
+//              loads Q, K and V tiles by TMA, page by page (a box is at most one
+//              page; lanes look the pages up and issue the boxes of a tile)
+//   warp 5     owns the tensor memory; one thread issues S = Q K^T (both from
+//              shared memory) and O += P V (P from tensor memory)
+//   warps 0-3  softmax, one thread per row, and the partials' stores
+// Tensor memory: S (128 columns fp32; P, bf16, over its first 64) and O (D).
+// The tensor core runs its instructions in order, so Q K^T of tile t + 1 may be
+// issued behind P V of tile t without waiting for it to have read P, and S(t +
+// 1) being complete says that P V of tile t is, too: O can then be rescaled.
+// O is rescaled only when a row's maximum has grown by more than 2^8.
+//
+// Keys that do not exist (past the end of the list, or on a page that is not
+// there) get probability 0, and their rows of V are zeroed in shared memory:
+// 0 * NaN would poison the row.
+constexpr int kTcRows = 128, kTcKeys = 128;
+constexpr int kTcSoftmaxWarps = 4, kTcProducerWarp = 4, kTcMmaWarp = 5;
+constexpr int kTcThreads = 192;
+constexpr int kPieceSlots = 4;
+constexpr uint64_t kWaitLimitNs = 4000000000ull;   // default: 4 s, far above any legitimate wait
+constexpr uint64_t kDrainLimitNs = 200000000ull;   // 0.2 s for the exit drain
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+
+template <int D>
+struct Tc {
+  static constexpr int NH = D / 64;                    // 64-column (128-byte) atoms of a row
+  static constexpr int VKEYS = 8192 / D;               // keys per V slot of 16 KB
+  // What fits beside the Q tile in half an SM's shared memory.  D = 128: one K
+  // slot (free once its Q K^T has run, refilled during the softmax) and three
+  // half-tile V slots.
+  static constexpr int NK = D == 128 ? 1 : 2, NV = D == 128 ? 3 : 4;
+  static constexpr uint32_t Q_BYTES = kTcRows * D * 2, K_BYTES = kTcKeys * D * 2, V_BYTES = 16384;
+  enum Bar {
+    Q_FULL, Q_EMPTY, S_FULL, P_FULL, O_FULL, DRAIN,
+    K_FULL, K_EMPTY = K_FULL + NK, V_FULL = K_EMPTY + NK, V_EMPTY = V_FULL + NV,
+    PIECE_FULL = V_EMPTY + NV, PIECE_EMPTY = PIECE_FULL + kPieceSlots,
+    COUNT = PIECE_EMPTY + kPieceSlots
+  };
+  static constexpr uint32_t TILES = Q_BYTES + NK * K_BYTES + NV * V_BYTES;
+  // Two CTAs fit an SM (228 KB, 1 KB of it reserved per CTA), three do not: each
+  // takes half of the tensor memory.
+  static constexpr uint32_t SMEM = TILES + 1024;
+  static_assert(SMEM <= 115712 && 3 * (SMEM + 1024) > 233472, "two CTAs per SM");
+};
+
+struct PieceRec {   // what the consumers need of a Piece
+  int32_t n_rows, kt0, kt1, n_keys, see0, off, shared, pad;
+  const int32_t *pages;
+  int64_t partial;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ f32x2 f2_add(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint64_t *bar,
+                                            int32_t x, int32_t y, int32_t z, int32_t w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(sm100::smem_u32(bar)), "r"(x), "r"(y), "r"(z),
+      "r"(w)
+      : "memory");
+}
+// Bounded wait on the way out: ignores the abort flag.
+__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
+  const uint64_t t0 = sm100::globaltimer_ns();
+  while (!sm100::mbar_try_wait(bar, parity)) {
+    if (sm100::globaltimer_ns() - t0 > kDrainLimitNs) return;
+  }
+}
+
+// Bit i: keys 16i .. 16i + 15 of the tile at k0 are on a page that is there.
+// Lanes 0..7 look one group up each.
+__device__ __forceinline__ uint32_t present_groups(const int32_t *pages, int k0, int n_keys,
+                                                   const PagedPool &pool, int lane) {
+  bool ok = false;
+  const int key = k0 + 16 * lane;
+  if (lane < 8 && key < n_keys) {
+    const int page = __ldg(pages + (key >> pool.page_shift));
+    ok = page >= 0 && page < pool.n_pages;
+  }
+  return __ballot_sync(kFull, ok) & 0xFFu;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 2)
+    attend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttendArgs a) {
+  using namespace sm100;
+  using C = Tc<D>;
+  constexpr uint32_t ATOM = 128 * 128;            // one 64-column atom of 128 rows
+  constexpr uint32_t VATOM = C::VKEYS * 128;      // ... of a V slot
+  constexpr uint32_t IDESC_QK = idesc_bf16_f32(kTcRows, kTcKeys, false);
+  constexpr uint32_t IDESC_PV = idesc_bf16_f32(kTcRows, D, true);
+  constexpr uint32_t TMEM_COLS = 256, COL_S = 0, COL_O = 128;
+
+  // Swizzled tiles sit on 1024-byte boundaries of shared memory: the dynamic
+  // part starts on one, having nothing static before it (checked below).
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t *sQ = smem, *sK = sQ + C::Q_BYTES, *sV = sK + C::NK * C::K_BYTES;
+  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::TILES);
+  PieceRec *ring = reinterpret_cast<PieceRec *>(bar + C::COUNT);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ring + kPieceSlots);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  static_assert(C::COUNT * 8 + kPieceSlots * sizeof(PieceRec) + 8 <= 1024, "barrier space");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const AttendPlan &p = a.plan;
+  const uint64_t limit = a.wait_limit_ns;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::COUNT; ++i) {
+      uint32_t n = 1;
+      if (i == C::P_FULL) n = kTcSoftmaxWarps * 32;
+      if (i >= C::PIECE_EMPTY) n = kTcSoftmaxWarps * 32 + 1;   // softmax threads and the issuer
+      mbar_init(&bar[i], n);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kTcMmaWarp) {
+    tmem_alloc(tmem_slot, TMEM_COLS);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_enter();
+  auto wait = [&](int b, uint32_t parity) -> bool {
+    return mbar_wait(&bar[b], parity, abort_flag, a.status, limit, DBSA_ERR_TIMEOUT);
+  };
+  // waits run by a whole warp
+  auto wait_warp = [&](int b, uint32_t parity) -> bool {
+    return __all_sync(kFull, wait(b, parity));
+  };
+
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicExch(a.status, DBSA_ERR_CUDA);
+  } else if (warp == kTcProducerWarp) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+    const int box = min(a.pool.page_size, C::VKEYS);   // rows per TMA box
+    const int n_boxes = kTcKeys / box * C::NH;         // of a K or V tile
+    const int brow = lane / C::NH * box;               // this lane's box: first key, atom
+    const int atom = lane % C::NH;
+    const uint32_t box_bytes = (uint32_t)box * 128;
+    const uint32_t k_dst = smem_u32(sK) + atom * ATOM + brow * 128;
+    const uint32_t v_dst = smem_u32(sV) + atom * VATOM + (brow % C::VKEYS) * 128;
+    const int v_part = brow / C::VKEYS;
+    uint32_t n_pieces = 0, kn = 0, vn = 0;
+    bool ok = true;
+    PieceWalk walk;
+    walk.init(blockIdx.x);
+    Piece pc;
+    if (a.withhold_tiles) {
+      // test hook: nothing is published or loaded, so every wait of the
+      // consumers runs out and raises the abort flag
+      const uint64_t t0 = globaltimer_ns();
+      while (!*abort_flag && globaltimer_ns() - t0 <= 2 * limit) __nanosleep(256);
+      ok = false;
+    }
+    while (ok && walk.next(p, a.batch, a.prefix_pages, pc)) {
+      const uint32_t slot = n_pieces % kPieceSlots;
+      if (n_pieces >= kPieceSlots &&
+          !(ok = wait_warp(C::PIECE_EMPTY + slot, (n_pieces / kPieceSlots - 1) & 1)))
+        break;
+      if (lane == 0) {
+        ring[slot] = {pc.n_rows, pc.kt0, pc.kt1, pc.n_keys, pc.see0,
+                      pc.off,    pc.shared, 0,   pc.pages,  pc.partial};
+        mbar_arrive(&bar[C::PIECE_FULL + slot]);
+      }
+      if (n_pieces > 0 && !(ok = wait_warp(C::Q_EMPTY, (n_pieces - 1) & 1))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bar[C::Q_FULL], C::Q_BYTES);
+#pragma unroll
+        for (int h = 0; h < C::NH; ++h)
+          tma_load_3d(sQ + h * ATOM, &tmQ, &bar[C::Q_FULL], h * 64, pc.row0, pc.c);
+      }
+      ++n_pieces;
+      for (int kt = pc.kt0; kt < pc.kt1; ++kt) {
+        const int k0 = kt * kTcKeys, key = k0 + brow;
+        int page = -1;
+        if (lane < n_boxes && key < pc.n_keys) page = __ldg(pc.pages + (key >> a.pool.page_shift));
+        const bool live = page >= 0 && page < a.pool.n_pages;
+        const int y = key & (a.pool.page_size - 1);
+        const uint32_t ks = kn % C::NK;
+        if (kn >= C::NK && !(ok = wait_warp(C::K_EMPTY + ks, (kn / C::NK - 1) & 1))) break;
+        uint32_t boxes = __popc(__ballot_sync(kFull, live));
+        if (lane == 0) mbar_arrive_expect_tx(&bar[C::K_FULL + ks], boxes * box_bytes);
+        __syncwarp();
+        if (live)
+          tma_load_4d(k_dst + ks * C::K_BYTES, &tmK, &bar[C::K_FULL + ks], atom * 64, y, pc.c, page);
+        ++kn;
+        const int parts = (min(kTcKeys, pc.n_keys - k0) + C::VKEYS - 1) / C::VKEYS;
+        for (int v = 0; v < parts; ++v, ++vn) {
+          const uint32_t vs = vn % C::NV;
+          if (vn >= C::NV && !(ok = wait_warp(C::V_EMPTY + vs, (vn / C::NV - 1) & 1))) break;
+          const bool mine = live && v_part == v;
+          boxes = __popc(__ballot_sync(kFull, mine));
+          if (lane == 0) mbar_arrive_expect_tx(&bar[C::V_FULL + vs], boxes * box_bytes);
+          __syncwarp();
+          if (mine)
+            tma_load_4d(v_dst + vs * C::V_BYTES, &tmV, &bar[C::V_FULL + vs], atom * 64, y, pc.c,
+                        page);
+        }
+        if (!ok) break;
+      }
+    }
+    // the end of the list
+    if (ok) {
+      const uint32_t slot = n_pieces % kPieceSlots;
+      if (n_pieces < kPieceSlots ||
+          (ok = wait_warp(C::PIECE_EMPTY + slot, (n_pieces / kPieceSlots - 1) & 1))) {
+        if (lane == 0) {
+          ring[slot].n_rows = 0;
+          mbar_arrive(&bar[C::PIECE_FULL + slot]);
+        }
+      }
+    }
+    // every load must have landed before the CTA exits
+    if (lane == 0) {
+      if (n_pieces > 0) drain_wait(&bar[C::Q_FULL], (n_pieces - 1) & 1);
+      for (uint32_t s = 0; s < C::NK; ++s)
+        if (kn > s) drain_wait(&bar[C::K_FULL + s], ((kn - 1 - s) / C::NK) & 1);
+      for (uint32_t s = 0; s < C::NV; ++s)
+        if (vn > s) drain_wait(&bar[C::V_FULL + s], ((vn - 1 - s) / C::NV) & 1);
+    }
+  } else if (warp == kTcMmaWarp) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t dV = sdesc_sw128(smem_u32(sV), VATOM, 1024);
+      uint32_t n_pieces = 0, kn = 0, vn = 0, tn = 0;
+      bool ok = true;
+      while (ok) {
+        const uint32_t slot = n_pieces % kPieceSlots;
+        if (!(ok = wait(C::PIECE_FULL + slot, (n_pieces / kPieceSlots) & 1))) break;
+        const int n_rows = ring[slot].n_rows, kt0 = ring[slot].kt0, kt1 = ring[slot].kt1;
+        const int n_keys = ring[slot].n_keys;
+        if (n_rows == 0) break;
+        mbar_arrive(&bar[C::PIECE_EMPTY + slot]);
+        if (!(ok = wait(C::Q_FULL, n_pieces & 1))) break;
+        ++n_pieces;
+        for (int kt = kt0; kt < kt1; ++kt, ++tn) {
+          const uint32_t ks = kn % C::NK;
+          if (!(ok = wait(C::K_FULL + ks, (kn / C::NK) & 1))) break;
+          ++kn;
+          tc_fence_after();
+          const uint64_t dk = dK + ks * (C::K_BYTES >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * ATOM + (kk & 3) * 32) >> 4;
+            mma_bf16_ss(tmem + COL_S, dQ + off, dk + off, IDESC_QK, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(&bar[C::S_FULL]);
+          mma_commit(&bar[C::K_EMPTY + ks]);
+          if (kt == kt1 - 1) mma_commit(&bar[C::Q_EMPTY]);
+          // P of this tile written, O rescaled or (first tile) read out
+          if (!(ok = wait(C::P_FULL, tn & 1))) break;
+          const int valid = min(kTcKeys, n_keys - kt * kTcKeys);
+          for (int v = 0; v * C::VKEYS < valid; ++v, ++vn) {
+            const uint32_t vs = vn % C::NV;
+            if (!(ok = wait(C::V_FULL + vs, (vn / C::NV) & 1))) break;
+            tc_fence_after();
+            const int steps = (min(C::VKEYS, valid - v * C::VKEYS) + 15) / 16;
+            const uint64_t dv = dV + vs * (C::V_BYTES >> 4);
+            const uint32_t pcol = tmem + COL_S + v * (C::VKEYS / 2);
+            const uint32_t first = kt > kt0 || v > 0 ? 1u : 0u;
+            if (steps == C::VKEYS / 16) {
+#pragma unroll
+              for (int kk = 0; kk < C::VKEYS / 16; ++kk)
+                mma_bf16_ts(tmem + COL_O, pcol + kk * 8, dv + kk * 128, IDESC_PV,
+                            kk > 0 ? 1u : first);
+            } else {
+              for (int kk = 0; kk < steps; ++kk)
+                mma_bf16_ts(tmem + COL_O, pcol + kk * 8, dv + kk * 128, IDESC_PV,
+                            kk > 0 ? 1u : first);
+            }
+            mma_commit(&bar[C::V_EMPTY + vs]);
+          }
+          if (!ok) break;
+          if (kt == kt1 - 1) mma_commit(&bar[C::O_FULL]);
+        }
+      }
+      // every instruction must be done before the tensor memory is given back
+      mma_commit(&bar[C::DRAIN]);
+      drain_wait(&bar[C::DRAIN], 0);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int row = warp * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const uint32_t t_s = tmem + lane_off + COL_S, t_o = tmem + lane_off + COL_O;
+    const float sl2 = a.scale_log2;
+    uint32_t n_pieces = 0, tn = 0, vn = 0;
+    bool ok = true;
+    while (ok) {
+      const uint32_t slot = n_pieces % kPieceSlots;
+      if (!(ok = wait_warp(C::PIECE_FULL + slot, (n_pieces / kPieceSlots) & 1))) break;
+      const PieceRec pc = ring[slot];
+      if (pc.n_rows == 0) break;
+      mbar_arrive(&bar[C::PIECE_EMPTY + slot]);
+      const bool idle = warp * 32 >= pc.n_rows;   // no row of this warp is one of the piece
+      const int seen = pc.shared ? pc.n_keys : min(pc.n_keys, pc.see0 + (pc.off + row) / p.g);
+      float m_ref = -INFINITY, l = 0.f;
+      for (int kt = pc.kt0; kt < pc.kt1; ++kt, ++tn) {
+        const int k0 = kt * kTcKeys, valid = min(kTcKeys, pc.n_keys - k0);
+        const uint32_t groups = present_groups(pc.pages, k0, pc.n_keys, a.pool, lane);
+        if (!(ok = wait_warp(C::S_FULL, tn & 1))) break;
+        tc_fence_after();
+        if (valid % 16 != 0 || groups != (1u << ((valid + 15) / 16)) - 1) {
+          // rows of V that P V will read and no key stands for: zero them.
+          // (S complete says that every earlier tile's V has been loaded and
+          // used, so these barriers are in this tile's phase or past it.)
+          for (int v = 0; v * C::VKEYS < valid; ++v) {
+            const uint32_t vs = (vn + v) % C::NV;
+            if (!(ok = wait_warp(C::V_FULL + vs, ((vn + v) / C::NV) & 1))) break;
+            uint8_t *tile = sV + vs * C::V_BYTES;
+            const int rows = (min(C::VKEYS, valid - v * C::VKEYS) + 15) / 16 * 16;
+            for (int i = threadIdx.x; i < rows * C::NH * 8; i += kTcSoftmaxWarps * 32) {
+              const int r = i / (C::NH * 8), key = v * C::VKEYS + r, x = i % (C::NH * 8);
+              if (key >= valid || ((groups >> (key >> 4)) & 1u) == 0)
+                *reinterpret_cast<uint4 *>(tile + (x >> 3) * VATOM + r * 128 + (x & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+          }
+          if (!ok) break;
+          fence_proxy_async_smem();
+        }
+        vn += (valid + C::VKEYS - 1) / C::VKEYS;
+        if (!idle) {
+          uint32_t s[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, s[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
+          // keys this row sees of the tile
+          const int lim = seen - k0;
+          if (__any_sync(kFull, lim < kTcKeys) || groups != 0xFFu) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (c * 32 + e >= lim || ((groups >> (c * 2 + e / 16)) & 1u) == 0)
+                  s[c][e] = __float_as_uint(-INFINITY);
+          }
+          float mt[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            mt[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+#pragma unroll
+            for (int e = 2; e < 32; e += 2)
+              mt[c] = max3(mt[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+          }
+          const float mx = max3(mt[0], mt[1], fmaxf(mt[2], mt[3])) * sl2;
+          if (kt == pc.kt0) {
+            m_ref = mx;
+          } else if (__any_sync(kFull, mx > m_ref + 8.f)) {
+            const float m_new = fmaxf(m_ref, mx);
+            const float f = m_new == -INFINITY ? 1.f : ex2(m_ref - m_new);
+            l *= f;
+            m_ref = m_new;
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(t_o + c * 16, o);
+              tmem_wait_ld16(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(t_o + c * 16, o);
+            }
+          }
+          const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+          const f32x2 sc2 = f2_pack(sl2, sl2), nmu2 = f2_pack(-mu, -mu);
+          f32x2 sum2[2] = {0ull, 0ull};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pw[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), sc2,
+                               nmu2),
+                        x0, x1);
+              const float p0 = ex2(x0), p1 = ex2(x1);
+              sum2[(e >> 1) & 1] = f2_add(sum2[(e >> 1) & 1], f2_pack(p0, p1));
+              __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+              pw[e >> 1] = *reinterpret_cast<uint32_t *>(&h);
+            }
+            tmem_st16(t_s + c * 16, pw);
+          }
+          tmem_wait_st();
+          float s0, s1, s2, s3;
+          f2_unpack(sum2[0], s0, s1);
+          f2_unpack(sum2[1], s2, s3);
+          l += (s0 + s1) + (s2 + s3);
+        }
+        tc_fence_before();
+        mbar_arrive(&bar[C::P_FULL]);
+      }
+      if (!ok) break;
+      if (!(ok = wait_warp(C::O_FULL, n_pieces & 1))) break;
+      ++n_pieces;
+      tc_fence_after();
+      if (!idle) {
+        float *dst = p.acc + (pc.partial + row) * D;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(t_o + c * 32, o);
+          tmem_wait_ld(o);
+          if (row < pc.n_rows) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4 *>(dst + c * 32 + e) =
+                  make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+        if (row < pc.n_rows) p.ml[pc.partial + row] = make_float2(m_ref, l);
+        tc_fence_before();   // O may be overwritten once P of the next piece is in
+      }
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == kTcMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &r) == cudaSuccess &&
+        r == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// bf16, boxes of 64 elements x `rows` rows, 128-byte swizzle.
+bool encode_map(CUtensorMap *m, const void *ptr, int rank, const cuuint64_t *dims,
+                const cuuint64_t *strides, int rows) {
+  const auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, one[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(ptr), dims, strides, box,
+             one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_tc(const AttendArgs &a, cudaStream_t st) {
+  using C = Tc<D>;
+  const AttendPlan &p = a.plan;
+  CUtensorMap mq, mk, mv;
+  const cuuint64_t qd[3] = {D, (cuuint64_t)p.rows, (cuuint64_t)p.Hkv};
+  const cuuint64_t qs[2] = {D * 2, (cuuint64_t)p.rows * D * 2};
+  const cuuint64_t kd[4] = {D, (cuuint64_t)a.pool.page_size, (cuuint64_t)p.Hkv,
+                            (cuuint64_t)a.pool.n_pages};
+  const cuuint64_t ks[3] = {D * 2, (cuuint64_t)a.pool.page_size * D * 2,
+                            (cuuint64_t)a.pool.page_stride * 2};
+  const int box = a.pool.page_size < C::VKEYS ? a.pool.page_size : C::VKEYS;
+  if (!encode_map(&mq, p.q_rot, 3, qd, qs, kTcRows) || !encode_map(&mk, a.pool.k, 4, kd, ks, box) ||
+      !encode_map(&mv, a.pool.v, 4, kd, ks, box))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = cudaFuncSetAttribute(
+      attend_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  if (e != cudaSuccess) return e;
+  AttendArgs b = a;
+  if (b.wait_limit_ns == 0) b.wait_limit_ns = kWaitLimitNs;
+  return pdl_launch(attend_tc_kernel<D>, dim3(p.n_ctas), dim3(kTcThreads), C::SMEM, st, mq, mk, mv,
+                    b);
 }
 
 }  // namespace
 
 AttendShape attend_shape(const dbsa_config *cfg) {
-  (void)cfg;
-  return {kSimpleRows, kSimpleKeys, 2 * 148};
+  if (cfg->dtype == DBSA_F32) return {kSimpleRows, kSimpleKeys, 2 * 148};
+  return {kTcRows, kTcKeys, 2 * 148};
 }
 
 cudaError_t launch_attend_pieces(const AttendArgs &a, int head_dim, bool f32, cudaStream_t st) {
-  if (head_dim == 128)
-    return f32 ? launch_simple<128, float>(a, st) : launch_simple<128, bf16>(a, st);
-  return f32 ? launch_simple<64, float>(a, st) : launch_simple<64, bf16>(a, st);
+  if (f32) return head_dim == 128 ? launch_simple<128>(a, st) : launch_simple<64>(a, st);
+  return head_dim == 128 ? launch_tc<128>(a, st) : launch_tc<64>(a, st);
 }
 
 }  // namespace dbsa

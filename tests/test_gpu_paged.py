@@ -215,6 +215,22 @@ def test_repeats_bit_for_bit_and_a_row_does_not_depend_on_the_batch_values(dtype
     assert torch.equal(b.attend(other)[0], got[0])
 
 
+def test_repeats_over_long_ragged_sequences():
+    """Ragged ends in most tiles (V rows zeroed while later loads are in
+    flight), several pieces per CTA: the same bits every time."""
+    cfg = config("gqa4", "bf16")
+    rng = np.random.default_rng(2)
+    b = Batch(cfg, 128, 1511, [1] * 48, rng.integers(100, 3000, 48).tolist(), seed=18).fill()
+    q = b.randn(b.rows, 32, 128)
+    tables, ws = b.tables(), b.workspace()
+    first = b.attend(q, tables=tables, workspace=ws)
+    want, tol = b.attention(q)
+    check(first, want, tol, "bf16", "long")
+    out = torch.empty_like(first)
+    for _ in range(30):
+        assert torch.equal(b.attend(q, out=out, tables=tables, workspace=ws), first)
+
+
 def test_offsets_beyond_32_bits():
     """Pages 2^31 elements apart (a view of one allocation)."""
     cfg = config("g5", "bf16")
@@ -344,3 +360,17 @@ def test_fixed_icl_from_the_stage1_cache():
             assert rel <= 8e-3, (step, s, rel)
             at += n
 
+
+
+def test_expired_waits_are_reported_and_the_next_call_is_right():
+    cfg = config("gqa4", "bf16")
+    b = Batch(cfg, 64, 700, [1] * 5, [1, 40, 200, 400, 65], seed=17).fill()
+    q = b.randn(b.rows, 32, 128)
+    want, tol = b.attention(q)
+    ws, tables = b.workspace(), b.tables()
+    dbsa.test_wait_expiry(1_000_000)
+    b.attend(q, tables=tables, workspace=ws)
+    assert dbsa.read_status(ws) == dbsa.ERR_TIMEOUT
+    out = b.attend(q, tables=tables, workspace=ws)
+    assert dbsa.read_status(ws) == dbsa.OK
+    check(out, want, tol, "bf16", "after an expired call")
