@@ -172,27 +172,28 @@ cudaError_t launch_simple(const AttendArgs &a, cudaStream_t st) {
 }
 
 // ------------------------------------------------------ tensor-core kernel
-// bf16 caches: tiles of 128 packed rows against 128 keys on tcgen05.
+// bf16 caches: tiles of 128 packed rows against 64 keys on tcgen05.
 //
 // Two CTAs per SM, 192 threads each, half of the SM's shared memory and tensor
-// memory each: while one CTA's softmax runs, the tensor core works for the
-// other.  Per CTA:
+// memory each, so that one CTA's waits are the other's work.  Per CTA:
 //   warp 4     walks the pieces, publishes each in a ring of kPieceSlots, and
 //              loads Q, K and V tiles by TMA, page by page (a box is at most one
 //              page; lanes look the pages up and issue the boxes of a tile)
 //   warp 5     owns the tensor memory; one thread issues S = Q K^T (both from
 //              shared memory) and O += P V (P from tensor memory)
 //   warps 0-3  softmax, one thread per row, and the partials' stores
-// Tensor memory: S (128 columns fp32; P, bf16, over its first 64) and O (D).
-// The tensor core runs its instructions in order, so Q K^T of tile t + 1 may be
-// issued behind P V of tile t without waiting for it to have read P, and S(t +
-// 1) being complete says that P V of tile t is, too: O can then be rescaled.
+// Tensor memory: two buffers of S (64 columns fp32; P, bf16, over the first 32
+// of its S) and O (D columns): all 256 of the CTA's half at D = 128.  Q K^T of
+// tile t + 1 runs while tile t is exponentiated, so the softmax warps find the
+// next scores waiting and the chain from one tile to the next is the softmax
+// alone.  The tensor core runs its instructions in order: Q K^T of tile t + 2
+// may be issued behind P V of tile t without waiting for it to have read P.
 // O is rescaled only when a row's maximum has grown by more than 2^8.
 //
 // Keys that do not exist (past the end of the list, or on a page that is not
 // there) get probability 0, and their rows of V are zeroed in shared memory:
 // 0 * NaN would poison the row.
-constexpr int kTcRows = 128, kTcKeys = 128;
+constexpr int kTcRows = 128, kTcKeys = 64;
 constexpr int kTcSoftmaxWarps = 4, kTcProducerWarp = 4, kTcMmaWarp = 5;
 constexpr int kTcThreads = 192;
 constexpr int kPieceSlots = 4;
@@ -203,19 +204,18 @@ constexpr uint32_t kFull = 0xFFFFFFFFu;
 template <int D>
 struct Tc {
   static constexpr int NH = D / 64;                    // 64-column (128-byte) atoms of a row
-  static constexpr int VKEYS = 8192 / D;               // keys per V slot of 16 KB
-  // What fits beside the Q tile in half an SM's shared memory.  D = 128: one K
-  // slot (free once its Q K^T has run, refilled during the softmax) and three
-  // half-tile V slots.
-  static constexpr int NK = D == 128 ? 1 : 2, NV = D == 128 ? 3 : 4;
-  static constexpr uint32_t Q_BYTES = kTcRows * D * 2, K_BYTES = kTcKeys * D * 2, V_BYTES = 16384;
+  static constexpr uint32_t Q_BYTES = kTcRows * D * 2, KV_BYTES = kTcKeys * D * 2;
+  // K and V tiles: what fits beside the Q tile in half an SM's shared memory.
+  // A K tile's slot is free once its Q K^T has run, a V tile's two softmaxes
+  // later.  Three V slots at least: the zeroing of V rows counts on it.
+  static constexpr int NK = D == 128 ? 2 : 6, NV = D == 128 ? 3 : 6;
   enum Bar {
-    Q_FULL, Q_EMPTY, S_FULL, P_FULL, O_FULL, DRAIN,
-    K_FULL, K_EMPTY = K_FULL + NK, V_FULL = K_EMPTY + NK, V_EMPTY = V_FULL + NV,
-    PIECE_FULL = V_EMPTY + NV, PIECE_EMPTY = PIECE_FULL + kPieceSlots,
+    Q_FULL, Q_EMPTY, S_FULL /* [buffer] */, P_FULL = S_FULL + 2 /* [buffer] */,
+    PV_DONE = P_FULL + 2 /* [buffer] */, DRAIN = PV_DONE + 2, K_FULL, K_EMPTY = K_FULL + NK, V_FULL = K_EMPTY + NK,
+    V_EMPTY = V_FULL + NV, PIECE_FULL = V_EMPTY + NV, PIECE_EMPTY = PIECE_FULL + kPieceSlots,
     COUNT = PIECE_EMPTY + kPieceSlots
   };
-  static constexpr uint32_t TILES = Q_BYTES + NK * K_BYTES + NV * V_BYTES;
+  static constexpr uint32_t TILES = Q_BYTES + (NK + NV) * KV_BYTES;
   // Two CTAs fit an SM (228 KB, 1 KB of it reserved per CTA), three do not: each
   // takes half of the tensor memory.
   static constexpr uint32_t SMEM = TILES + 1024;
@@ -261,16 +261,16 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
 }
 
 // Bit i: keys 16i .. 16i + 15 of the tile at k0 are on a page that is there.
-// Lanes 0..7 look one group up each.
+// Lanes 0..3 look one group up each.
 __device__ __forceinline__ uint32_t present_groups(const int32_t *pages, int k0, int n_keys,
                                                    const PagedPool &pool, int lane) {
   bool ok = false;
   const int key = k0 + 16 * lane;
-  if (lane < 8 && key < n_keys) {
+  if (lane < kTcKeys / 16 && key < n_keys) {
     const int page = __ldg(pages + (key >> pool.page_shift));
     ok = page >= 0 && page < pool.n_pages;
   }
-  return __ballot_sync(kFull, ok) & 0xFFu;
+  return __ballot_sync(kFull, ok);
 }
 
 template <int D>
@@ -279,16 +279,16 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttendArgs a) {
   using namespace sm100;
   using C = Tc<D>;
-  constexpr uint32_t ATOM = 128 * 128;            // one 64-column atom of 128 rows
-  constexpr uint32_t VATOM = C::VKEYS * 128;      // ... of a V slot
+  constexpr uint32_t QATOM = kTcRows * 128;       // one 64-column atom of the Q tile
+  constexpr uint32_t ATOM = kTcKeys * 128;        // ... of a K or V tile
   constexpr uint32_t IDESC_QK = idesc_bf16_f32(kTcRows, kTcKeys, false);
   constexpr uint32_t IDESC_PV = idesc_bf16_f32(kTcRows, D, true);
-  constexpr uint32_t TMEM_COLS = 256, COL_S = 0, COL_O = 128;
+  constexpr uint32_t TMEM_COLS = 256, COL_S = 0, COL_O = 2 * kTcKeys;
 
   // Swizzled tiles sit on 1024-byte boundaries of shared memory: the dynamic
   // part starts on one, having nothing static before it (checked below).
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t *sQ = smem, *sK = sQ + C::Q_BYTES, *sV = sK + C::NK * C::K_BYTES;
+  uint8_t *sQ = smem, *sK = sQ + C::Q_BYTES, *sV = sK + C::NK * C::KV_BYTES;
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::TILES);
   PieceRec *ring = reinterpret_cast<PieceRec *>(bar + C::COUNT);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ring + kPieceSlots);
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::COUNT; ++i) {
       uint32_t n = 1;
-      if (i == C::P_FULL) n = kTcSoftmaxWarps * 32;
+      if (i == C::P_FULL || i == C::P_FULL + 1) n = kTcSoftmaxWarps * 32;
       if (i >= C::PIECE_EMPTY) n = kTcSoftmaxWarps * 32 + 1;   // softmax threads and the issuer
       mbar_init(&bar[i], n);
     }
@@ -334,14 +334,12 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
     }
-    const int box = min(a.pool.page_size, C::VKEYS);   // rows per TMA box
+    const int box = min(a.pool.page_size, kTcKeys);    // rows per TMA box
     const int n_boxes = kTcKeys / box * C::NH;         // of a K or V tile
     const int brow = lane / C::NH * box;               // this lane's box: first key, atom
     const int atom = lane % C::NH;
     const uint32_t box_bytes = (uint32_t)box * 128;
-    const uint32_t k_dst = smem_u32(sK) + atom * ATOM + brow * 128;
-    const uint32_t v_dst = smem_u32(sV) + atom * VATOM + (brow % C::VKEYS) * 128;
-    const int v_part = brow / C::VKEYS;
+    const uint32_t dst = atom * ATOM + brow * 128;
     uint32_t n_pieces = 0, kn = 0, vn = 0;
     bool ok = true;
     PieceWalk walk;
@@ -369,36 +367,42 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         mbar_arrive_expect_tx(&bar[C::Q_FULL], C::Q_BYTES);
 #pragma unroll
         for (int h = 0; h < C::NH; ++h)
-          tma_load_3d(sQ + h * ATOM, &tmQ, &bar[C::Q_FULL], h * 64, pc.row0, pc.c);
+          tma_load_3d(sQ + h * QATOM, &tmQ, &bar[C::Q_FULL], h * 64, pc.row0, pc.c);
       }
       ++n_pieces;
-      for (int kt = pc.kt0; kt < pc.kt1; ++kt) {
-        const int k0 = kt * kTcKeys, key = k0 + brow;
-        int page = -1;
-        if (lane < n_boxes && key < pc.n_keys) page = __ldg(pc.pages + (key >> a.pool.page_shift));
-        const bool live = page >= 0 && page < a.pool.n_pages;
-        const int y = key & (a.pool.page_size - 1);
-        const uint32_t ks = kn % C::NK;
-        if (kn >= C::NK && !(ok = wait_warp(C::K_EMPTY + ks, (kn / C::NK - 1) & 1))) break;
-        uint32_t boxes = __popc(__ballot_sync(kFull, live));
-        if (lane == 0) mbar_arrive_expect_tx(&bar[C::K_FULL + ks], boxes * box_bytes);
-        __syncwarp();
-        if (live)
-          tma_load_4d(k_dst + ks * C::K_BYTES, &tmK, &bar[C::K_FULL + ks], atom * 64, y, pc.c, page);
-        ++kn;
-        const int parts = (min(kTcKeys, pc.n_keys - k0) + C::VKEYS - 1) / C::VKEYS;
-        for (int v = 0; v < parts; ++v, ++vn) {
+      // in the order of their use: K of a tile, then V of the tile before
+      int page = -1, next = -1, y = 0, next_y = 0;
+      for (int kt = pc.kt0; kt <= pc.kt1; ++kt) {
+        if (kt < pc.kt1) {
+          const int key = kt * kTcKeys + brow;
+          next = -1;
+          if (lane < n_boxes && key < pc.n_keys)
+            next = __ldg(pc.pages + (key >> a.pool.page_shift));
+          if (next >= a.pool.n_pages) next = -1;
+          next_y = key & (a.pool.page_size - 1);
+          const uint32_t ks = kn % C::NK;
+          if (kn >= C::NK && !(ok = wait_warp(C::K_EMPTY + ks, (kn / C::NK - 1) & 1))) break;
+          const uint32_t boxes = __popc(__ballot_sync(kFull, next >= 0));
+          if (lane == 0) mbar_arrive_expect_tx(&bar[C::K_FULL + ks], boxes * box_bytes);
+          __syncwarp();
+          if (next >= 0)
+            tma_load_4d(smem_u32(sK) + ks * C::KV_BYTES + dst, &tmK, &bar[C::K_FULL + ks],
+                        atom * 64, next_y, pc.c, next);
+          ++kn;
+        }
+        if (kt > pc.kt0) {
           const uint32_t vs = vn % C::NV;
           if (vn >= C::NV && !(ok = wait_warp(C::V_EMPTY + vs, (vn / C::NV - 1) & 1))) break;
-          const bool mine = live && v_part == v;
-          boxes = __popc(__ballot_sync(kFull, mine));
+          const uint32_t boxes = __popc(__ballot_sync(kFull, page >= 0));
           if (lane == 0) mbar_arrive_expect_tx(&bar[C::V_FULL + vs], boxes * box_bytes);
           __syncwarp();
-          if (mine)
-            tma_load_4d(v_dst + vs * C::V_BYTES, &tmV, &bar[C::V_FULL + vs], atom * 64, y, pc.c,
-                        page);
+          if (page >= 0)
+            tma_load_4d(smem_u32(sV) + vs * C::KV_BYTES + dst, &tmV, &bar[C::V_FULL + vs],
+                        atom * 64, y, pc.c, page);
+          ++vn;
         }
-        if (!ok) break;
+        page = next;
+        y = next_y;
       }
     }
     // the end of the list
@@ -425,8 +429,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     if (lane == 0) {
       const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024);
-      const uint64_t dV = sdesc_sw128(smem_u32(sV), VATOM, 1024);
-      uint32_t n_pieces = 0, kn = 0, vn = 0, tn = 0;
+      const uint64_t dV = sdesc_sw128(smem_u32(sV), ATOM, 1024);
+      uint32_t n_pieces = 0;
+      uint32_t ks = 0, kph = 0, vs = 0, vph = 0;   // K and V slots and their phases
+      uint32_t sn = 0, tn = 0;                     // tiles Q K^T and P V have been issued for
       bool ok = true;
       while (ok) {
         const uint32_t slot = n_pieces % kPieceSlots;
@@ -437,45 +443,53 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         mbar_arrive(&bar[C::PIECE_EMPTY + slot]);
         if (!(ok = wait(C::Q_FULL, n_pieces & 1))) break;
         ++n_pieces;
-        for (int kt = kt0; kt < kt1; ++kt, ++tn) {
-          const uint32_t ks = kn % C::NK;
-          if (!(ok = wait(C::K_FULL + ks, (kn / C::NK) & 1))) break;
-          ++kn;
-          tc_fence_after();
-          const uint64_t dk = dK + ks * (C::K_BYTES >> 4);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * ATOM + (kk & 3) * 32) >> 4;
-            mma_bf16_ss(tmem + COL_S, dQ + off, dk + off, IDESC_QK, kk > 0 ? 1u : 0u);
-          }
-          mma_commit(&bar[C::S_FULL]);
-          mma_commit(&bar[C::K_EMPTY + ks]);
-          if (kt == kt1 - 1) mma_commit(&bar[C::Q_EMPTY]);
-          // P of this tile written, O rescaled or (first tile) read out
-          if (!(ok = wait(C::P_FULL, tn & 1))) break;
-          const int valid = min(kTcKeys, n_keys - kt * kTcKeys);
-          for (int v = 0; v * C::VKEYS < valid; ++v, ++vn) {
-            const uint32_t vs = vn % C::NV;
-            if (!(ok = wait(C::V_FULL + vs, (vn / C::NV) & 1))) break;
+        for (int kt = kt0; kt <= kt1; ++kt) {
+          if (kt < kt1) {   // S of this tile, while the one before is exponentiated
+            if (!(ok = wait(C::K_FULL + ks, kph))) break;
             tc_fence_after();
-            const int steps = (min(C::VKEYS, valid - v * C::VKEYS) + 15) / 16;
-            const uint64_t dv = dV + vs * (C::V_BYTES >> 4);
-            const uint32_t pcol = tmem + COL_S + v * (C::VKEYS / 2);
-            const uint32_t first = kt > kt0 || v > 0 ? 1u : 0u;
-            if (steps == C::VKEYS / 16) {
+            const uint64_t dk = dK + ks * (C::KV_BYTES >> 4);
+            const uint32_t d = tmem + COL_S + (sn & 1) * kTcKeys;
 #pragma unroll
-              for (int kk = 0; kk < C::VKEYS / 16; ++kk)
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_bf16_ss(d, dQ + (((kk >> 2) * QATOM + (kk & 3) * 32) >> 4),
+                          dk + (((kk >> 2) * ATOM + (kk & 3) * 32) >> 4), IDESC_QK,
+                          kk > 0 ? 1u : 0u);
+            mma_commit(&bar[C::S_FULL + (sn & 1)]);
+            mma_commit(&bar[C::K_EMPTY + ks]);
+            if (kt == kt1 - 1) mma_commit(&bar[C::Q_EMPTY]);
+            ++sn;
+            if (++ks == C::NK) {
+              ks = 0;
+              kph ^= 1;
+            }
+          }
+          if (kt > kt0) {   // O += P V of the tile before
+            if (!(ok = wait(C::V_FULL + vs, vph))) break;
+            // P written, and O rescaled or (first tile) read out
+            if (!(ok = wait(C::P_FULL + (tn & 1), (tn >> 1) & 1))) break;
+            tc_fence_after();
+            const uint64_t dv = dV + vs * (C::KV_BYTES >> 4);
+            const uint32_t pcol = tmem + COL_S + (tn & 1) * kTcKeys;
+            const uint32_t first = kt > kt0 + 1 ? 1u : 0u;
+            const int valid = n_keys - (kt - 1) * kTcKeys;
+            if (valid > kTcKeys - 16) {
+#pragma unroll
+              for (int kk = 0; kk < kTcKeys / 16; ++kk)
                 mma_bf16_ts(tmem + COL_O, pcol + kk * 8, dv + kk * 128, IDESC_PV,
                             kk > 0 ? 1u : first);
             } else {
-              for (int kk = 0; kk < steps; ++kk)
+              for (int kk = 0; kk * 16 < valid; ++kk)
                 mma_bf16_ts(tmem + COL_O, pcol + kk * 8, dv + kk * 128, IDESC_PV,
                             kk > 0 ? 1u : first);
             }
+            mma_commit(&bar[C::PV_DONE + (tn & 1)]);
             mma_commit(&bar[C::V_EMPTY + vs]);
+            ++tn;
+            if (++vs == C::NV) {
+              vs = 0;
+              vph ^= 1;
+            }
           }
-          if (!ok) break;
-          if (kt == kt1 - 1) mma_commit(&bar[C::O_FULL]);
         }
       }
       // every instruction must be done before the tensor memory is given back
@@ -486,9 +500,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     // ------------------------------------------------------------ softmax
     const int row = warp * 32 + lane;
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-    const uint32_t t_s = tmem + lane_off + COL_S, t_o = tmem + lane_off + COL_O;
+    const uint32_t t_o = tmem + lane_off + COL_O;
     const float sl2 = a.scale_log2;
-    uint32_t n_pieces = 0, tn = 0, vn = 0;
+    uint32_t n_pieces = 0, tn = 0;
     bool ok = true;
     while (ok) {
       const uint32_t slot = n_pieces % kPieceSlots;
@@ -496,45 +510,43 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       const PieceRec pc = ring[slot];
       if (pc.n_rows == 0) break;
       mbar_arrive(&bar[C::PIECE_EMPTY + slot]);
+      ++n_pieces;
       const bool idle = warp * 32 >= pc.n_rows;   // no row of this warp is one of the piece
       const int seen = pc.shared ? pc.n_keys : min(pc.n_keys, pc.see0 + (pc.off + row) / p.g);
       float m_ref = -INFINITY, l = 0.f;
       for (int kt = pc.kt0; kt < pc.kt1; ++kt, ++tn) {
         const int k0 = kt * kTcKeys, valid = min(kTcKeys, pc.n_keys - k0);
         const uint32_t groups = present_groups(pc.pages, k0, pc.n_keys, a.pool, lane);
-        if (!(ok = wait_warp(C::S_FULL, tn & 1))) break;
+        const uint32_t t_s = tmem + lane_off + COL_S + (tn & 1) * kTcKeys;
+        if (!(ok = wait_warp(C::S_FULL + (tn & 1), (tn >> 1) & 1))) break;
         tc_fence_after();
         if (valid % 16 != 0 || groups != (1u << ((valid + 15) / 16)) - 1) {
-          // rows of V that P V will read and no key stands for: zero them.
-          // (S complete says that every earlier tile's V has been loaded and
-          // used, so these barriers are in this tile's phase or past it.)
-          for (int v = 0; v * C::VKEYS < valid; ++v) {
-            const uint32_t vs = (vn + v) % C::NV;
-            if (!(ok = wait_warp(C::V_FULL + vs, ((vn + v) / C::NV) & 1))) break;
-            uint8_t *tile = sV + vs * C::V_BYTES;
-            const int rows = (min(C::VKEYS, valid - v * C::VKEYS) + 15) / 16 * 16;
-            for (int i = threadIdx.x; i < rows * C::NH * 8; i += kTcSoftmaxWarps * 32) {
-              const int r = i / (C::NH * 8), key = v * C::VKEYS + r, x = i % (C::NH * 8);
-              if (key >= valid || ((groups >> (key >> 4)) & 1u) == 0)
-                *reinterpret_cast<uint4 *>(tile + (x >> 3) * VATOM + r * 128 + (x & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
-            }
+          // Rows of V that P V will read and no key stands for: zero them.  S of
+          // tile t being complete says that P V of tile t - 2 is, so with three
+          // slots or more this one's barrier is in this tile's phase or past it.
+          const uint32_t vs = tn % C::NV;
+          if (!(ok = wait_warp(C::V_FULL + vs, (tn / C::NV) & 1))) break;
+          uint8_t *tile = sV + vs * C::KV_BYTES;
+          const int rows = (valid + 15) / 16 * 16;
+          for (int i = threadIdx.x; i < rows * C::NH * 8; i += kTcSoftmaxWarps * 32) {
+            const int r = i / (C::NH * 8), x = i % (C::NH * 8);
+            if (r >= valid || ((groups >> (r >> 4)) & 1u) == 0)
+              *reinterpret_cast<uint4 *>(tile + (x >> 3) * ATOM + r * 128 + (x & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
           }
-          if (!ok) break;
           fence_proxy_async_smem();
         }
-        vn += (valid + C::VKEYS - 1) / C::VKEYS;
         if (!idle) {
-          uint32_t s[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, s[c]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
+          uint32_t s[2][32];
+          tmem_ld32(t_s, s[0]);
+          tmem_ld32(t_s + 32, s[1]);
+          tmem_wait_ld(s[0]);
+          tmem_wait_ld(s[1]);
           // keys this row sees of the tile
           const int lim = seen - k0;
-          if (__any_sync(kFull, lim < kTcKeys) || groups != 0xFFu) {
+          if (__any_sync(kFull, lim < kTcKeys) || groups != 0xFu) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (c * 32 + e >= lim || ((groups >> (c * 2 + e / 16)) & 1u) == 0)
@@ -543,15 +555,19 @@ __global__ void __launch_bounds__(kTcThreads, 2)
           float mt[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            mt[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+            const uint32_t *x = &s[c >> 1][(c & 1) * 16];
+            mt[c] = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
 #pragma unroll
-            for (int e = 2; e < 32; e += 2)
-              mt[c] = max3(mt[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+            for (int e = 2; e < 16; e += 2)
+              mt[c] = max3(mt[c], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
           }
           const float mx = max3(mt[0], mt[1], fmaxf(mt[2], mt[3])) * sl2;
           if (kt == pc.kt0) {
             m_ref = mx;
           } else if (__any_sync(kFull, mx > m_ref + 8.f)) {
+            // O must hold the tiles before this one
+            if (!(ok = wait_warp(C::PV_DONE + ((tn - 1) & 1), ((tn - 1) >> 1) & 1))) break;
+            tc_fence_after();
             const float m_new = fmaxf(m_ref, mx);
             const float f = m_new == -INFINITY ? 1.f : ex2(m_ref - m_new);
             l *= f;
@@ -570,7 +586,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
           const f32x2 sc2 = f2_pack(sl2, sl2), nmu2 = f2_pack(-mu, -mu);
           f32x2 sum2[2] = {0ull, 0ull};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 2; ++c) {
             uint32_t pw[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
@@ -592,11 +608,12 @@ __global__ void __launch_bounds__(kTcThreads, 2)
           l += (s0 + s1) + (s2 + s3);
         }
         tc_fence_before();
-        mbar_arrive(&bar[C::P_FULL]);
+        mbar_arrive(&bar[C::P_FULL + (tn & 1)]);
       }
       if (!ok) break;
-      if (!(ok = wait_warp(C::O_FULL, n_pieces & 1))) break;
-      ++n_pieces;
+      // P V of the last tile (that of the tile two before it, on the same
+      // barrier, is done since the last S is)
+      if (!(ok = wait_warp(C::PV_DONE + ((tn - 1) & 1), ((tn - 1) >> 1) & 1))) break;
       tc_fence_after();
       if (!idle) {
         float *dst = p.acc + (pc.partial + row) * D;
@@ -662,7 +679,7 @@ cudaError_t launch_tc(const AttendArgs &a, cudaStream_t st) {
                             (cuuint64_t)a.pool.n_pages};
   const cuuint64_t ks[3] = {D * 2, (cuuint64_t)a.pool.page_size * D * 2,
                             (cuuint64_t)a.pool.page_stride * 2};
-  const int box = a.pool.page_size < C::VKEYS ? a.pool.page_size : C::VKEYS;
+  const int box = a.pool.page_size < kTcKeys ? a.pool.page_size : kTcKeys;
   if (!encode_map(&mq, p.q_rot, 3, qd, qs, kTcRows) || !encode_map(&mk, a.pool.k, 4, kd, ks, box) ||
       !encode_map(&mv, a.pool.v, 4, kd, ks, box))
     return cudaErrorInvalidValue;
