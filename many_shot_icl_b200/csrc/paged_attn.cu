@@ -174,28 +174,31 @@ cudaError_t launch_simple(const AttendArgs &a, cudaStream_t st) {
 // ------------------------------------------------------ tensor-core kernel
 // bf16 caches: tiles of 128 packed rows against 64 keys on tcgen05.
 //
-// Two CTAs per SM, 192 threads each, half of the SM's shared memory and tensor
+// Two CTAs per SM, 224 threads each, half of the SM's shared memory and tensor
 // memory each, so that one CTA's waits are the other's work.  Per CTA:
 //   warp 4     walks the pieces, publishes each in a ring of kPieceSlots, and
 //              loads Q, K and V tiles by TMA, page by page (a box is at most one
 //              page; lanes look the pages up and issue the boxes of a tile)
 //   warp 5     owns the tensor memory; one thread issues S = Q K^T (both from
-//              shared memory) and O += P V (P from tensor memory)
+//              shared memory)
+//   warp 6     one thread issues O += P V (P from tensor memory)
 //   warps 0-3  softmax, one thread per row, and the partials' stores
 // Tensor memory: two buffers of S (64 columns fp32; P, bf16, over the first 32
 // of its S) and O (D columns): all 256 of the CTA's half at D = 128.  Q K^T of
 // tile t + 1 runs while tile t is exponentiated, so the softmax warps find the
 // next scores waiting and the chain from one tile to the next is the softmax
-// alone.  The tensor core runs its instructions in order: Q K^T of tile t + 2
-// may be issued behind P V of tile t without waiting for it to have read P.
+// alone.  An issuing thread spends ~125 cycles on each wait, met or not, and as
+// much on each commit, so there are two of them and few barriers: S_FULL also
+// says that the tile's K slot is free, PV_DONE that its V slot and its S buffer
+// are.
 // O is rescaled only when a row's maximum has grown by more than 2^8.
 //
 // Keys that do not exist (past the end of the list, or on a page that is not
 // there) get probability 0, and their rows of V are zeroed in shared memory:
 // 0 * NaN would poison the row.
 constexpr int kTcRows = 128, kTcKeys = 64;
-constexpr int kTcSoftmaxWarps = 4, kTcProducerWarp = 4, kTcMmaWarp = 5;
-constexpr int kTcThreads = 192;
+constexpr int kTcSoftmaxWarps = 4, kTcProducerWarp = 4, kTcQkWarp = 5, kTcPvWarp = 6;
+constexpr int kTcThreads = 224;
 constexpr int kPieceSlots = 4;
 constexpr uint64_t kWaitLimitNs = 4000000000ull;   // default: 4 s, far above any legitimate wait
 constexpr uint64_t kDrainLimitNs = 200000000ull;   // 0.2 s for the exit drain
@@ -205,20 +208,19 @@ template <int D>
 struct Tc {
   static constexpr int NH = D / 64;                    // 64-column (128-byte) atoms of a row
   static constexpr uint32_t Q_BYTES = kTcRows * D * 2, KV_BYTES = kTcKeys * D * 2;
-  // K and V tiles: what fits beside the Q tile in half an SM's shared memory.
-  // A K tile's slot is free once its Q K^T has run, a V tile's two softmaxes
-  // later.  Three V slots at least: the zeroing of V rows counts on it.
-  static constexpr int NK = D == 128 ? 2 : 6, NV = D == 128 ? 3 : 6;
+  // K and V tiles.  K slots go with the S buffers; V slots are one more, since
+  // a tile's V is used a softmax later.
+  static constexpr int NK = 2, NV = 3;
   enum Bar {
-    Q_FULL, Q_EMPTY, S_FULL /* [buffer] */, P_FULL = S_FULL + 2 /* [buffer] */,
-    PV_DONE = P_FULL + 2 /* [buffer] */, DRAIN = PV_DONE + 2, K_FULL, K_EMPTY = K_FULL + NK, V_FULL = K_EMPTY + NK,
-    V_EMPTY = V_FULL + NV, PIECE_FULL = V_EMPTY + NV, PIECE_EMPTY = PIECE_FULL + kPieceSlots,
-    COUNT = PIECE_EMPTY + kPieceSlots
+    Q_FULL, Q_EMPTY, DRAIN_QK, DRAIN_PV, S_FULL /* [K slot, S buffer] */,
+    P_FULL = S_FULL + NK /* [S buffer] */, K_FULL = P_FULL + NK, V_FULL = K_FULL + NK,
+    PV_DONE = V_FULL + NV /* [V slot] */, PIECE_FULL = PV_DONE + NV,
+    PIECE_EMPTY = PIECE_FULL + kPieceSlots, COUNT = PIECE_EMPTY + kPieceSlots
   };
   static constexpr uint32_t TILES = Q_BYTES + (NK + NV) * KV_BYTES;
   // Two CTAs fit an SM (228 KB, 1 KB of it reserved per CTA), three do not: each
   // takes half of the tensor memory.
-  static constexpr uint32_t SMEM = TILES + 1024;
+  static constexpr uint32_t NEED = TILES + 1024, SMEM = NEED > 80 * 1024 ? NEED : 80 * 1024;
   static_assert(SMEM <= 115712 && 3 * (SMEM + 1024) > 233472, "two CTAs per SM");
 };
 
@@ -260,17 +262,11 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
   }
 }
 
-// Bit i: keys 16i .. 16i + 15 of the tile at k0 are on a page that is there.
-// Lanes 0..3 look one group up each.
-__device__ __forceinline__ uint32_t present_groups(const int32_t *pages, int k0, int n_keys,
-                                                   const PagedPool &pool, int lane) {
-  bool ok = false;
+// Page of keys 16 * lane .. of the tile at k0 (lanes 0..3), -1 if there is none.
+__device__ __forceinline__ int group_page(const int32_t *pages, int k0, int n_keys,
+                                          const PagedPool &pool, int lane) {
   const int key = k0 + 16 * lane;
-  if (lane < kTcKeys / 16 && key < n_keys) {
-    const int page = __ldg(pages + (key >> pool.page_shift));
-    ok = page >= 0 && page < pool.n_pages;
-  }
-  return __ballot_sync(kFull, ok);
+  return lane < kTcKeys / 16 && key < n_keys ? __ldg(pages + (key >> pool.page_shift)) : -1;
 }
 
 template <int D>
@@ -302,13 +298,13 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     for (int i = 0; i < C::COUNT; ++i) {
       uint32_t n = 1;
       if (i == C::P_FULL || i == C::P_FULL + 1) n = kTcSoftmaxWarps * 32;
-      if (i >= C::PIECE_EMPTY) n = kTcSoftmaxWarps * 32 + 1;   // softmax threads and the issuer
+      if (i >= C::PIECE_EMPTY) n = kTcSoftmaxWarps * 32 + 2;   // softmax threads and the issuers
       mbar_init(&bar[i], n);
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kTcMmaWarp) {
+  if (warp == kTcQkWarp) {
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
     tc_fence_before();
@@ -381,7 +377,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
           if (next >= a.pool.n_pages) next = -1;
           next_y = key & (a.pool.page_size - 1);
           const uint32_t ks = kn % C::NK;
-          if (kn >= C::NK && !(ok = wait_warp(C::K_EMPTY + ks, (kn / C::NK - 1) & 1))) break;
+          if (kn >= C::NK && !(ok = wait_warp(C::S_FULL + ks, (kn / C::NK - 1) & 1))) break;
           const uint32_t boxes = __popc(__ballot_sync(kFull, next >= 0));
           if (lane == 0) mbar_arrive_expect_tx(&bar[C::K_FULL + ks], boxes * box_bytes);
           __syncwarp();
@@ -392,7 +388,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         }
         if (kt > pc.kt0) {
           const uint32_t vs = vn % C::NV;
-          if (vn >= C::NV && !(ok = wait_warp(C::V_EMPTY + vs, (vn / C::NV - 1) & 1))) break;
+          if (vn >= C::NV && !(ok = wait_warp(C::PV_DONE + vs, (vn / C::NV - 1) & 1))) break;
           const uint32_t boxes = __popc(__ballot_sync(kFull, page >= 0));
           if (lane == 0) mbar_arrive_expect_tx(&bar[C::V_FULL + vs], boxes * box_bytes);
           __syncwarp();
@@ -424,15 +420,16 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       for (uint32_t s = 0; s < C::NV; ++s)
         if (vn > s) drain_wait(&bar[C::V_FULL + s], ((vn - 1 - s) / C::NV) & 1);
     }
-  } else if (warp == kTcMmaWarp) {
-    // ------------------------------------------------------------ MMA issuer
+  } else if (warp == kTcQkWarp || warp == kTcPvWarp) {
+    // ------------------------------------------------------------ MMA issuers
     if (lane == 0) {
+      const bool qk = warp == kTcQkWarp;
       const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024);
       const uint64_t dV = sdesc_sw128(smem_u32(sV), ATOM, 1024);
-      uint32_t n_pieces = 0;
-      uint32_t ks = 0, kph = 0, vs = 0, vph = 0;   // K and V slots and their phases
-      uint32_t sn = 0, tn = 0;                     // tiles Q K^T and P V have been issued for
+      uint32_t n_pieces = 0, tn = 0;
+      // slot and phase of tile tn's V (P V) or of V two tiles before (Q K^T)
+      uint32_t vs = 0, vph = 0;
       bool ok = true;
       while (ok) {
         const uint32_t slot = n_pieces % kPieceSlots;
@@ -441,37 +438,38 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         const int n_keys = ring[slot].n_keys;
         if (n_rows == 0) break;
         mbar_arrive(&bar[C::PIECE_EMPTY + slot]);
-        if (!(ok = wait(C::Q_FULL, n_pieces & 1))) break;
+        if (qk && !(ok = wait(C::Q_FULL, n_pieces & 1))) break;
         ++n_pieces;
-        for (int kt = kt0; kt <= kt1; ++kt) {
-          if (kt < kt1) {   // S of this tile, while the one before is exponentiated
-            if (!(ok = wait(C::K_FULL + ks, kph))) break;
+        for (int kt = kt0; kt < kt1; ++kt, ++tn) {
+          const uint32_t b = tn & 1, ph = (tn >> 1) & 1;
+          if (qk) {
+            if (!(ok = wait(C::K_FULL + b, ph))) break;
+            if (tn >= 2) {   // P of the tile that had this S buffer has been used
+              if (!(ok = wait(C::PV_DONE + vs, vph))) break;
+              if (++vs == C::NV) {
+                vs = 0;
+                vph ^= 1;
+              }
+            }
             tc_fence_after();
-            const uint64_t dk = dK + ks * (C::KV_BYTES >> 4);
-            const uint32_t d = tmem + COL_S + (sn & 1) * kTcKeys;
+            const uint64_t dk = dK + b * (C::KV_BYTES >> 4);
+            const uint32_t d = tmem + COL_S + b * kTcKeys;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               mma_bf16_ss(d, dQ + (((kk >> 2) * QATOM + (kk & 3) * 32) >> 4),
                           dk + (((kk >> 2) * ATOM + (kk & 3) * 32) >> 4), IDESC_QK,
                           kk > 0 ? 1u : 0u);
-            mma_commit(&bar[C::S_FULL + (sn & 1)]);
-            mma_commit(&bar[C::K_EMPTY + ks]);
+            mma_commit(&bar[C::S_FULL + b]);
             if (kt == kt1 - 1) mma_commit(&bar[C::Q_EMPTY]);
-            ++sn;
-            if (++ks == C::NK) {
-              ks = 0;
-              kph ^= 1;
-            }
-          }
-          if (kt > kt0) {   // O += P V of the tile before
+          } else {
             if (!(ok = wait(C::V_FULL + vs, vph))) break;
             // P written, and O rescaled or (first tile) read out
-            if (!(ok = wait(C::P_FULL + (tn & 1), (tn >> 1) & 1))) break;
+            if (!(ok = wait(C::P_FULL + b, ph))) break;
             tc_fence_after();
             const uint64_t dv = dV + vs * (C::KV_BYTES >> 4);
-            const uint32_t pcol = tmem + COL_S + (tn & 1) * kTcKeys;
-            const uint32_t first = kt > kt0 + 1 ? 1u : 0u;
-            const int valid = n_keys - (kt - 1) * kTcKeys;
+            const uint32_t pcol = tmem + COL_S + b * kTcKeys;
+            const uint32_t first = kt > kt0 ? 1u : 0u;
+            const int valid = n_keys - kt * kTcKeys;
             if (valid > kTcKeys - 16) {
 #pragma unroll
               for (int kk = 0; kk < kTcKeys / 16; ++kk)
@@ -482,9 +480,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 mma_bf16_ts(tmem + COL_O, pcol + kk * 8, dv + kk * 128, IDESC_PV,
                             kk > 0 ? 1u : first);
             }
-            mma_commit(&bar[C::PV_DONE + (tn & 1)]);
-            mma_commit(&bar[C::V_EMPTY + vs]);
-            ++tn;
+            mma_commit(&bar[C::PV_DONE + vs]);
             if (++vs == C::NV) {
               vs = 0;
               vph ^= 1;
@@ -493,8 +489,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         }
       }
       // every instruction must be done before the tensor memory is given back
-      mma_commit(&bar[C::DRAIN]);
-      drain_wait(&bar[C::DRAIN], 0);
+      mma_commit(&bar[qk ? C::DRAIN_QK : C::DRAIN_PV]);
+      drain_wait(&bar[qk ? C::DRAIN_QK : C::DRAIN_PV], 0);
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -514,16 +510,19 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       const bool idle = warp * 32 >= pc.n_rows;   // no row of this warp is one of the piece
       const int seen = pc.shared ? pc.n_keys : min(pc.n_keys, pc.see0 + (pc.off + row) / p.g);
       float m_ref = -INFINITY, l = 0.f;
+      int page = group_page(pc.pages, pc.kt0 * kTcKeys, pc.n_keys, a.pool, lane);
       for (int kt = pc.kt0; kt < pc.kt1; ++kt, ++tn) {
         const int k0 = kt * kTcKeys, valid = min(kTcKeys, pc.n_keys - k0);
-        const uint32_t groups = present_groups(pc.pages, k0, pc.n_keys, a.pool, lane);
+        // bit i: keys 16i .. 16i + 15 of the tile are on a page that is there
+        const uint32_t groups = __ballot_sync(kFull, page >= 0 && page < a.pool.n_pages);
+        page = group_page(pc.pages, k0 + kTcKeys, pc.n_keys, a.pool, lane);   // the next tile's
         const uint32_t t_s = tmem + lane_off + COL_S + (tn & 1) * kTcKeys;
         if (!(ok = wait_warp(C::S_FULL + (tn & 1), (tn >> 1) & 1))) break;
         tc_fence_after();
         if (valid % 16 != 0 || groups != (1u << ((valid + 15) / 16)) - 1) {
           // Rows of V that P V will read and no key stands for: zero them.  S of
           // tile t being complete says that P V of tile t - 2 is, so with three
-          // slots or more this one's barrier is in this tile's phase or past it.
+          // slots this one's barrier is in this tile's phase or past it.
           const uint32_t vs = tn % C::NV;
           if (!(ok = wait_warp(C::V_FULL + vs, (tn / C::NV) & 1))) break;
           uint8_t *tile = sV + vs * C::KV_BYTES;
@@ -566,7 +565,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             m_ref = mx;
           } else if (__any_sync(kFull, mx > m_ref + 8.f)) {
             // O must hold the tiles before this one
-            if (!(ok = wait_warp(C::PV_DONE + ((tn - 1) & 1), ((tn - 1) >> 1) & 1))) break;
+            if (!(ok = wait_warp(C::PV_DONE + (tn - 1) % C::NV, ((tn - 1) / C::NV) & 1))) break;
             tc_fence_after();
             const float m_new = fmaxf(m_ref, mx);
             const float f = m_new == -INFINITY ? 1.f : ex2(m_ref - m_new);
@@ -611,9 +610,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         mbar_arrive(&bar[C::P_FULL + (tn & 1)]);
       }
       if (!ok) break;
-      // P V of the last tile (that of the tile two before it, on the same
+      // P V of the last tile (that of the tile three before it, on the same
       // barrier, is done since the last S is)
-      if (!(ok = wait_warp(C::PV_DONE + ((tn - 1) & 1), ((tn - 1) >> 1) & 1))) break;
+      if (!(ok = wait_warp(C::PV_DONE + (tn - 1) % C::NV, ((tn - 1) / C::NV) & 1))) break;
       tc_fence_after();
       if (!idle) {
         float *dst = p.acc + (pc.partial + row) * D;
@@ -636,7 +635,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   }
   __syncwarp();
   __syncthreads();
-  if (warp == kTcMmaWarp) {
+  if (warp == kTcQkWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
   }
