@@ -13,6 +13,7 @@ import os
 from dataclasses import dataclass
 
 import numpy as np
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdbsa.so")
@@ -174,7 +175,6 @@ def _dp(t) -> int | None:
 
 
 def _stream(stream) -> int:
-    import torch
     s = torch.cuda.current_stream() if stream is None else stream
     return s.cuda_stream
 
@@ -353,76 +353,71 @@ def _refuse(msg: str):
     raise DbsaError(ERR_INVALID_ARG, msg)
 
 
-class _Call:
-    """Device and stream of a call on tensors of one device: that device is
-    made current for the call when it is not, and the stream defaults to its
-    current one."""
-
-    def __init__(self, device, stream):
-        import torch
-        self._guard = None
-        if device.index != torch.cuda.current_device():
-            self._guard = torch.cuda.device(device)
-        self._device, self._torch, self.stream = device, torch, stream
-
-    def __enter__(self) -> int:
-        if self._guard is not None:
-            self._guard.__enter__()
-        s = self._torch.cuda.current_stream(self._device) if self.stream is None else self.stream
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
-
-
-def _on_device(device, **tensors):
-    for name, t in tensors.items():
-        if not t.is_cuda or t.device != device:
-            _refuse("%s must be on the CUDA device of the pages (%s)" % (name, device))
+def _run(fn, index: int, stream, *args):
+    """Call fn(*args, stream) with device `index` current, on its current
+    stream unless one is given.  (The raw-stream query: the public stream
+    object costs 2 us, a quarter of a short call.)"""
+    cuda = torch.cuda
+    st = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == cuda.current_device():
+        status = fn(*args, st)
+    else:
+        with cuda.device(index):
+            status = fn(*args, st)
+    if status != OK:
+        _check(status)
 
 
 def _strides(t):
     """Row and head stride of [rows][heads][d]; 0 for a dimension of one."""
-    return tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in (0, 1))
+    n, h, _ = t.shape
+    a, b, _ = t.stride()
+    return (a if n > 1 else 0), (b if h > 1 else 0)
 
 
-def _paged_args(cfg: DbsaConfig, k_pages, v_pages, page_table, row_ptr, seq_lens, tables, n_rows):
-    """The cache and batch structs of a call, after checking the tensors."""
-    import torch
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+def _torch_dtype(cfg: DbsaConfig):
+    return torch.float32 if cfg.dtype == "f32" else torch.bfloat16
+
+
+def _paged_args(cfg: DbsaConfig, k_pages, v_pages, page_table, row_ptr, seq_lens, tables, n_rows,
+                more):
+    """The cache and batch structs of a call and its device's index, after
+    checking the tensors; `more`: the call's other tensors, by name."""
+    shape, dtype = k_pages.shape, _torch_dtype(cfg)
+    if len(shape) != 4 or v_pages.shape != shape:
         _refuse("pages must be [n_pages][n_kv_heads][page_size][head_dim], keys and values alike")
-    n_pages, hkv, page_size, d = k_pages.shape
+    n_pages, hkv, page_size, d = shape
     if hkv != cfg.n_kv_heads or d != cfg.head_dim:
         _refuse("pages of %d heads of %d elements; cfg has %d of %d"
                 % (hkv, d, cfg.n_kv_heads, cfg.head_dim))
-    stride = k_pages.stride(0) if n_pages > 1 else hkv * page_size * d
-    dtype = torch.float32 if cfg.dtype == "f32" else torch.bfloat16
-    for t in (k_pages, v_pages):
-        st = t.stride()
-        if (t.dtype != dtype or st[3] != 1 or st[2] != d or (hkv > 1 and st[1] != page_size * d)
-                or (n_pages > 1 and st[0] != stride)):
-            _refuse("pages must be %s, contiguous inside a page, with one page stride" % dtype)
-    n_seqs = seq_lens.shape[0]
-    if (row_ptr.dtype != torch.int32 or seq_lens.dtype != torch.int32
-            or page_table.dtype != torch.int32 or seq_lens.dim() != 1
-            or row_ptr.shape != (n_seqs + 1,) or page_table.dim() != 2
-            or page_table.shape[0] != n_seqs):
+    st = k_pages.stride()
+    if (k_pages.dtype != dtype or v_pages.dtype != dtype or st[3] != 1 or st[2] != d
+            or (hkv > 1 and st[1] != page_size * d) or v_pages.stride() != st):
+        _refuse("pages must be %s, contiguous inside a page, with one page stride" % dtype)
+    i32 = torch.int32
+    n_seqs, table = seq_lens.numel(), page_table.shape
+    if (row_ptr.dtype != i32 or seq_lens.dtype != i32 or page_table.dtype != i32
+            or len(table) != 2 or table[0] != n_seqs or row_ptr.numel() != n_seqs + 1):
         _refuse("row_ptr [n_seqs + 1], seq_lens [n_seqs] and page_table [n_seqs][width] must be "
                 "int32")
-    width = page_table.shape[1]
+    pt = page_table.stride()
     if (not row_ptr.is_contiguous() or not seq_lens.is_contiguous()
-            or (width > 1 and page_table.stride(1) != 1)):
+            or (table[1] > 1 and pt[1] != 1)):
         _refuse("row_ptr and seq_lens must be contiguous, and the rows of page_table")
     if not tables.is_contiguous():
         _refuse("tables must be contiguous")
-    _on_device(k_pages.device, k_pages=k_pages, v_pages=v_pages, page_table=page_table,
-               row_ptr=row_ptr, seq_lens=seq_lens, tables=tables)
-    cache = PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), stride, n_pages, page_size)
-    table_stride = page_table.stride(0) if n_seqs > 1 else max(width, 1)
+    index = k_pages.get_device()
+    if index < 0 or not (index == v_pages.get_device() == page_table.get_device()
+                         == row_ptr.get_device() == seq_lens.get_device() == tables.get_device()):
+        _refuse("pages, page_table, row_ptr, seq_lens and tables must be on one CUDA device")
+    for name in more:
+        if more[name].get_device() != index:
+            _refuse("%s must be on the CUDA device of the pages" % name)
+    cache = PagedCache(k_pages.data_ptr(), v_pages.data_ptr(),
+                       st[0] if n_pages > 1 else hkv * page_size * d, n_pages, page_size)
     batch = PagedBatch(n_seqs, n_rows, row_ptr.data_ptr(), seq_lens.data_ptr(),
-                       page_table.data_ptr(), width, table_stride)
-    return cache, batch, dtype
+                       page_table.data_ptr(), table[1], pt[0] if n_seqs > 1 else max(table[1], 1))
+    return cache, batch, index
 
 
 def rope_tables_size(cfg: DbsaConfig, n_pos: int) -> int:
@@ -433,12 +428,11 @@ def rope_tables_size(cfg: DbsaConfig, n_pos: int) -> int:
 def rope_tables(cfg: DbsaConfig, n_pos: int, buf, stream=None):
     """Angle tables for positions [0, n_pos) into buf (uint8 device tensor of
     rope_tables_size() bytes), for paged_append and shared_prefix_attend."""
-    if not buf.is_cuda or not buf.is_contiguous():
+    if buf.get_device() < 0 or not buf.is_contiguous():
         _refuse("buf must be a contiguous CUDA tensor")
     c = cfg.c()
-    with _Call(buf.device, stream) as st:
-        _check(load().dbsa_rope_tables(ctypes.byref(c), n_pos, _dp(buf),
-                                       buf.numel() * buf.element_size(), st))
+    _run(load().dbsa_rope_tables, buf.get_device(), stream, ctypes.byref(c), n_pos, _dp(buf),
+         buf.numel() * buf.element_size())
 
 
 def paged_append(cfg: DbsaConfig, k, v, k_pages, v_pages, page_table, row_ptr, seq_lens, tables,
@@ -446,20 +440,19 @@ def paged_append(cfg: DbsaConfig, k, v, k_pages, v_pages, page_table, row_ptr, s
     """Append the rows k, v [n_rows][n_kv_heads][head_dim] (any row and head
     stride) of a batch to their sequences' pages, keys rotated at pos0 + their
     index in the sequence (see dbsa_paged_append)."""
-    cache, batch, dtype = _paged_args(cfg, k_pages, v_pages, page_table, row_ptr, seq_lens, tables,
-                                      k.shape[0])
-    _on_device(k_pages.device, k=k, v=v)
-    shape = (k.shape[0], cfg.n_kv_heads, cfg.head_dim)
-    for t in (k, v):
-        if t.dtype != dtype or t.shape != shape or t.stride(2) != 1:
-            _refuse("k and v must be %s [n_rows][n_kv_heads][head_dim] with contiguous elements"
-                    % dtype)
+    shape = k.shape
+    cache, batch, index = _paged_args(cfg, k_pages, v_pages, page_table, row_ptr, seq_lens, tables,
+                                      shape[0], {"k": k, "v": v})
+    dtype = _torch_dtype(cfg)
+    if (k.dtype != dtype or v.dtype != dtype or shape != v.shape or len(shape) != 3
+            or shape[1] != cfg.n_kv_heads or shape[2] != cfg.head_dim or k.stride(2) != 1
+            or v.stride(2) != 1):
+        _refuse("k and v must be %s [n_rows][n_kv_heads][head_dim] with contiguous elements"
+                % dtype)
     c = cfg.c()
-    with _Call(k_pages.device, stream) as st:
-        _check(load().dbsa_paged_append(
-            ctypes.byref(c), _dp(k), *_strides(k), _dp(v), *_strides(v),
-            ctypes.byref(cache), ctypes.byref(batch), pos0, _dp(tables),
-            tables.numel() * tables.element_size(), st))
+    _run(load().dbsa_paged_append, index, stream, ctypes.byref(c), k.data_ptr(), *_strides(k),
+         v.data_ptr(), *_strides(v), ctypes.byref(cache), ctypes.byref(batch), pos0,
+         tables.data_ptr(), tables.numel() * tables.element_size())
 
 
 def shared_prefix_workspace_size(cfg: DbsaConfig, n_seqs: int, n_rows: int,
@@ -475,28 +468,30 @@ def shared_prefix_attend(cfg: DbsaConfig, q, k_pages, v_pages, prefix_pages, pre
     over a shared prefix and, causally, each row's own sequence, into out of
     the same shape, contiguous (see dbsa_shared_prefix_attend).  prefix_pages
     may be None when prefix_len is 0."""
-    import torch
-    cache, batch, dtype = _paged_args(cfg, k_pages, v_pages, page_table, row_ptr, seq_lens, tables,
-                                      q.shape[0])
-    _on_device(k_pages.device, q=q, out=out, workspace=workspace)
-    shape = (q.shape[0], cfg.n_q_heads, cfg.head_dim)
-    if (q.dtype != dtype or q.shape != shape or q.stride(2) != 1
-            or (cfg.n_q_heads > 1 and q.stride(1) != cfg.head_dim)):
+    shape = q.shape
+    more = {"q": q, "out": out, "workspace": workspace}
+    if prefix_len > 0:
+        if prefix_pages is None:
+            _refuse("prefix_pages is None")
+        more["prefix_pages"] = prefix_pages
+    cache, batch, index = _paged_args(cfg, k_pages, v_pages, page_table, row_ptr, seq_lens, tables,
+                                      shape[0], more)
+    dtype = _torch_dtype(cfg)
+    d = cfg.head_dim
+    st = q.stride()
+    if (q.dtype != dtype or len(shape) != 3 or shape[1] != cfg.n_q_heads or shape[2] != d
+            or st[2] != 1 or (shape[1] > 1 and st[1] != d)):
         _refuse("q must be %s [n_rows][n_q_heads][head_dim], each row contiguous" % dtype)
     if out.dtype != dtype or out.shape != shape or not out.is_contiguous():
         _refuse("out must be %s, contiguous, of q's shape" % dtype)
     if not workspace.is_contiguous():
         _refuse("workspace must be contiguous")
     if prefix_len > 0:
-        if prefix_pages is None:
-            _refuse("prefix_pages is None")
-        _on_device(k_pages.device, prefix_pages=prefix_pages)
         if (prefix_pages.dtype != torch.int32 or not prefix_pages.is_contiguous()
                 or prefix_pages.numel() * cache.page_size < prefix_len):
             _refuse("prefix_pages must be contiguous int32, one entry per page of the prefix")
     c = cfg.c()
-    with _Call(k_pages.device, stream) as st:
-        _check(load().dbsa_shared_prefix_attend(
-            ctypes.byref(c), _dp(q), _strides(q)[0], ctypes.byref(cache), _dp(prefix_pages),
-            prefix_len, ctypes.byref(batch), _dp(tables), tables.numel() * tables.element_size(),
-            _dp(out), _dp(workspace), workspace.numel() * workspace.element_size(), st))
+    _run(load().dbsa_shared_prefix_attend, index, stream, ctypes.byref(c), q.data_ptr(),
+         st[0] if shape[0] > 1 else 0, ctypes.byref(cache), _dp(prefix_pages), prefix_len,
+         ctypes.byref(batch), tables.data_ptr(), tables.numel() * tables.element_size(),
+         out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
