@@ -150,6 +150,12 @@ struct PieceWalk {
     e = 0;
   }
 
+  // Whether the first piece is one of the prefix; such pieces are known from the
+  // call's arguments, without the plan in device memory.
+  __device__ __forceinline__ bool starts_shared(const AttendPlan &p) const {
+    return item < (int64_t)p.n_groups * p.n_row_tiles;
+  }
+
   __device__ bool next(const AttendPlan &p, const PagedBatch &b, const int32_t *prefix_pages,
                        Piece &o) {
     if (!own) {

@@ -297,8 +297,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::COUNT; ++i) {
       uint32_t n = 1;
-      if (i == C::P_FULL || i == C::P_FULL + 1) n = kTcSoftmaxWarps * 32;
-      if (i >= C::PIECE_EMPTY) n = kTcSoftmaxWarps * 32 + 2;   // softmax threads and the issuers
+      if (i == C::P_FULL || i == C::P_FULL + 1) n = kTcSoftmaxWarps;
+      if (i >= C::PIECE_EMPTY) n = kTcSoftmaxWarps + 2;   // softmax warps and the issuers
       mbar_init(&bar[i], n);
     }
     *abort_flag = 0;
@@ -312,9 +312,14 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_enter();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   auto wait = [&](int b, uint32_t parity) -> bool {
     return mbar_wait(&bar[b], parity, abort_flag, a.status, limit, DBSA_ERR_TIMEOUT);
+  };
+  // one arrival for a whole warp, behind all its lanes' accesses
+  auto arrive_warp = [&](int b) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[b]);
   };
   // waits run by a whole warp
   auto wait_warp = [&](int b, uint32_t parity) -> bool {
@@ -341,13 +346,34 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     PieceWalk walk;
     walk.init(blockIdx.x);
     Piece pc;
+    // The producer alone waits for the kernel before (which rotated the queries
+    // and built the plan of the own tokens), and only when it needs them: the
+    // first tiles of a prefix piece are loaded before that.  Their pages are
+    // complete: the kernel before let this one start only after it had itself
+    // waited for everything before it in the stream.
+    bool entered = false, hold_q = false;
+    auto enter = [&]() {
+      if (!entered) asm volatile("griddepcontrol.wait;" ::: "memory");
+      entered = true;
+    };
+    auto load_q = [&]() {
+      enter();
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bar[C::Q_FULL], C::Q_BYTES);
+#pragma unroll
+        for (int h = 0; h < C::NH; ++h)
+          tma_load_3d(sQ + h * QATOM, &tmQ, &bar[C::Q_FULL], h * 64, pc.row0, pc.c);
+      }
+    };
     if (a.withhold_tiles) {
+      enter();
       // test hook: nothing is published or loaded, so every wait of the
       // consumers runs out and raises the abort flag
       const uint64_t t0 = globaltimer_ns();
       while (!*abort_flag && globaltimer_ns() - t0 <= 2 * limit) __nanosleep(256);
       ok = false;
     }
+    if (!walk.starts_shared(p)) enter();
     while (ok && walk.next(p, a.batch, a.prefix_pages, pc)) {
       const uint32_t slot = n_pieces % kPieceSlots;
       if (n_pieces >= kPieceSlots &&
@@ -359,16 +385,16 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         mbar_arrive(&bar[C::PIECE_FULL + slot]);
       }
       if (n_pieces > 0 && !(ok = wait_warp(C::Q_EMPTY, (n_pieces - 1) & 1))) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bar[C::Q_FULL], C::Q_BYTES);
-#pragma unroll
-        for (int h = 0; h < C::NH; ++h)
-          tma_load_3d(sQ + h * QATOM, &tmQ, &bar[C::Q_FULL], h * 64, pc.row0, pc.c);
-      }
+      hold_q = !entered;
+      if (!hold_q) load_q();
       ++n_pieces;
       // in the order of their use: K of a tile, then V of the tile before
       int page = -1, next = -1, y = 0, next_y = 0;
       for (int kt = pc.kt0; kt <= pc.kt1; ++kt) {
+        if (hold_q && kt == pc.kt0 + C::NK) {   // no K slot is left to fill
+          load_q();
+          hold_q = false;
+        }
         if (kt < pc.kt1) {
           const int key = kt * kTcKeys + brow;
           next = -1;
@@ -400,6 +426,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         page = next;
         y = next_y;
       }
+      if (hold_q) load_q();
     }
     // the end of the list
     if (ok) {
@@ -505,7 +532,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       if (!(ok = wait_warp(C::PIECE_FULL + slot, (n_pieces / kPieceSlots) & 1))) break;
       const PieceRec pc = ring[slot];
       if (pc.n_rows == 0) break;
-      mbar_arrive(&bar[C::PIECE_EMPTY + slot]);
+      arrive_warp(C::PIECE_EMPTY + slot);
       ++n_pieces;
       const bool idle = warp * 32 >= pc.n_rows;   // no row of this warp is one of the piece
       const int seen = pc.shared ? pc.n_keys : min(pc.n_keys, pc.see0 + (pc.off + row) / p.g);
@@ -607,7 +634,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
           l += (s0 + s1) + (s2 + s3);
         }
         tc_fence_before();
-        mbar_arrive(&bar[C::P_FULL + (tn & 1)]);
+        arrive_warp(C::P_FULL + (tn & 1));
       }
       if (!ok) break;
       // P V of the last tile (that of the tile three before it, on the same
