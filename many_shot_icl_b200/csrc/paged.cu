@@ -50,18 +50,18 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs<T> a) {
   const int i0 = (threadIdx.x % CP) * 8;
   if (row >= a.batch.n_rows) return;
   const T *ks = a.k + row * a.k_row + c * a.k_head, *vs = a.v + row * a.v_row + c * a.v_head;
-  const int2 st = row_token(a.batch, row);
-  if (st.x < 0 || st.y < 0) return;
-  const int page = __ldg(a.batch.page_table + (int64_t)st.x * a.batch.table_stride +
-                         (st.y >> a.pool.page_shift));
+  const RowToken t = row_token(a.batch, row);
+  if (t.seq < 0 || t.token < 0) return;
+  const int page = __ldg(a.batch.page_table + (int64_t)t.seq * a.batch.table_stride +
+                         (t.token >> a.pool.page_shift));
   if (page < 0 || page >= a.pool.n_pages) return;
   const int64_t dst =
       page * a.pool.page_stride +
-      ((int64_t)c * a.pool.page_size + (st.y & (a.pool.page_size - 1))) * D + i0;
+      ((int64_t)c * a.pool.page_size + (t.token & (a.pool.page_size - 1))) * D + i0;
   float lo[8], hi[8], cs[8], sn[8];
   load8(ks + i0, lo);
   load8(ks + H + i0, hi);
-  rope_cs8(a.rope, a.pos0 + st.y, i0, H, cs, sn);
+  rope_cs8(a.rope, a.pos0 + t.token, i0, H, cs, sn);
   rotate8(lo, hi, cs, sn);
   T *kd = static_cast<T *>(a.pool.k) + dst, *vd = static_cast<T *>(a.pool.v) + dst;
   store8(kd, lo);
@@ -94,47 +94,76 @@ __device__ int64_t block_scan(int64_t x, int64_t *total) {
   return before + inc - x;
 }
 
+// Units of one row tile of a sequence: the key tiles its last row sees, for
+// every KV head.
+__device__ __forceinline__ int64_t tile_units(const AttendPlan &p, const SeqRows &s, int rt) {
+  const int64_t last = min((int64_t)(rt + 1) * p.tile_rows, (int64_t)s.n * p.g) - 1;
+  const int64_t seen = min((int64_t)s.len, s.len - s.n + 1 + last / p.g);
+  return seen > 0 ? (seen + p.tile_keys - 1) / p.tile_keys * p.Hkv : 0;
+}
+
 // The own-token entries and their units, by one block.
 __device__ void build_plan(const AttendPlan &p, const PagedBatch &b) {
-  int64_t at = 0, total;
+  const int tid = threadIdx.x;
+  int64_t at = 0, units = 0, total;
+  SeqRows s = {0, 0, 0};
+  int more = 0;   // whether a sequence has several row tiles
   for (int s0 = 0; s0 < b.n_seqs; s0 += 256) {
-    const int s = s0 + threadIdx.x;
-    int64_t n = 0;
-    if (s < b.n_seqs) n = ((int64_t)seq_rows(b, s).n * p.g + p.tile_rows - 1) / p.tile_rows;
-    const int64_t first = at + block_scan(n, &total);
-    // more entries than max_entries need a decreasing row_ptr; none is written
-    if (s < b.n_seqs) p.first_entry[s] = (int32_t)min(first, (int64_t)p.max_entries);
-    at += total;
-  }
-  const int32_t ne = (int32_t)min(at, (int64_t)p.max_entries);
-  if (threadIdx.x == 0) {
-    p.first_entry[b.n_seqs] = ne;
-    *p.n_entries = ne;
-  }
-  __syncthreads();
-  int64_t units = 0;
-  for (int e0 = 0; e0 < ne; e0 += 256) {
-    const int e = e0 + threadIdx.x;
-    int64_t n = 0;
-    if (e < ne) {
-      int lo = 0, hi = b.n_seqs;   // the first sequence whose entries end past e
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (p.first_entry[mid + 1] > e) hi = mid; else lo = mid + 1;
-      }
-      const int rt = e - p.first_entry[lo];
-      p.entry[e] = make_int2(lo, rt);
-      const SeqRows s = seq_rows(b, lo);
-      // keys the last row of the tile sees
-      const int64_t end = min((int64_t)(rt + 1) * p.tile_rows, (int64_t)s.n * p.g) - 1;
-      const int64_t seen = min((int64_t)s.len, s.len - s.n + 1 + end / p.g);
-      n = seen > 0 ? (seen + p.tile_keys - 1) / p.tile_keys * p.Hkv : 0;
+    if (s0 + tid < b.n_seqs) {
+      s = seq_rows(b, s0 + tid);
+      more |= (int64_t)s.n * p.g > p.tile_rows;
     }
-    const int64_t first = units + block_scan(n, &total);
-    if (e < ne) p.units[e] = first;
-    units += total;
   }
-  if (threadIdx.x == 0) p.units[ne] = units;
+  const int single = !__syncthreads_or(more);
+  if (single) {   // entry = sequence (decode steps, short prompts): one pass
+    for (int s0 = 0; s0 < b.n_seqs; s0 += 256) {
+      const int e = s0 + tid;
+      int64_t n = 0;
+      if (e < b.n_seqs) {
+        if (b.n_seqs > 256) s = seq_rows(b, e);
+        p.entry[e] = make_int2(e, 0);
+        if (s.n > 0) n = tile_units(p, s, 0);
+      }
+      const int64_t first = units + block_scan(n, &total);
+      if (e < b.n_seqs) p.units[e] = first;
+      units += total;
+    }
+    at = b.n_seqs;
+  } else {
+    for (int s0 = 0; s0 < b.n_seqs; s0 += 256) {
+      const int i = s0 + tid;
+      int64_t n = 0;
+      if (i < b.n_seqs) n = ((int64_t)seq_rows(b, i).n * p.g + p.tile_rows - 1) / p.tile_rows;
+      const int64_t first = at + block_scan(n, &total);
+      // more entries than max_entries need a decreasing row_ptr; none is written
+      if (i < b.n_seqs) p.first_entry[i] = (int32_t)min(first, (int64_t)p.max_entries);
+      at += total;
+    }
+    at = min(at, (int64_t)p.max_entries);
+    if (tid == 0) p.first_entry[b.n_seqs] = (int32_t)at;
+    __syncthreads();
+    for (int e0 = 0; e0 < at; e0 += 256) {
+      const int e = e0 + tid;
+      int64_t n = 0;
+      if (e < at) {
+        int lo = 0, hi = b.n_seqs;   // the first sequence whose entries end past e
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (p.first_entry[mid + 1] > e) hi = mid; else lo = mid + 1;
+        }
+        const int rt = e - p.first_entry[lo];
+        p.entry[e] = make_int2(lo, rt);
+        n = tile_units(p, seq_rows(b, lo), rt);
+      }
+      const int64_t first = units + block_scan(n, &total);
+      if (e < at) p.units[e] = first;
+      units += total;
+    }
+  }
+  if (tid == 0) {
+    p.units[at] = units;
+    *p.head = {units, (int32_t)at, single, 0};
+  }
 }
 
 // Queries rotated at their positions and packed per KV head (one rounding to
@@ -153,33 +182,46 @@ __global__ void __launch_bounds__(256) attend_prep_kernel(const AttendArgs a) {
   const int row = (blockIdx.x / p.Hkv) * (256 / CP) + threadIdx.x / CP;
   const int cp = threadIdx.x % CP, i0 = cp * 8;
   if (row >= a.batch.n_rows) return;
-  const int2 st = row_token(a.batch, row);
-  if (c == 0 && cp == 0) p.row_info[row] = st;
-  const bool live = st.x >= 0 && st.y >= 0;   // other rows: finite, never used
-  float cs[8], sn[8];
-  rope_cs8(a.rope, live ? (int64_t)p.prefix_len + st.y : 0, i0, H, cs, sn);
-  const T *src = static_cast<const T *>(a.q) + row * a.q_row_stride + (int64_t)c * p.g * D;
-  T *dst = static_cast<T *>(p.q_rot) + ((int64_t)c * p.rows + (int64_t)row * p.g) * D;
-#pragma unroll 4
-  for (int hl = 0; hl < p.g; ++hl) {
-    float lo[8], hi[8];
-    load8(src + (int64_t)hl * D + i0, lo);
-    load8(src + (int64_t)hl * D + H + i0, hi);
-    rotate8(lo, hi, cs, sn);
-    if (!live) {
+  const T *src = static_cast<const T *>(a.q) + row * a.q_row_stride + (int64_t)c * p.g * D + i0;
+  T *dst = static_cast<T *>(p.q_rot) + ((int64_t)c * p.rows + (int64_t)row * p.g) * D + i0;
+  // two heads at a time, the first two requested before the row's position
+  float lo[2][8], hi[2][8], cs[8], sn[8];
+  auto load = [&](int hl) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) lo[e] = hi[e] = 0.f;
+    for (int k = 0; k < 2; ++k)
+      if (hl + k < p.g) {
+        load8(src + (int64_t)(hl + k) * D, lo[k]);
+        load8(src + (int64_t)(hl + k) * D + H, hi[k]);
+      }
+  };
+  load(0);
+  const RowToken t = row_token(a.batch, row);
+  if (c == 0 && cp == 0) p.row_info[row] = make_int4(t.seq, t.token, t.rows.row0, t.rows.n);
+  const bool live = t.seq >= 0 && t.token >= 0;   // other rows: finite, never used
+  rope_cs8(a.rope, live ? (int64_t)p.prefix_len + t.token : 0, i0, H, cs, sn);
+  for (int hl = 0; hl < p.g; hl += 2) {
+    if (hl > 0) load(hl);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (hl + k >= p.g) break;
+      rotate8(lo[k], hi[k], cs, sn);
+      if (!live) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) lo[k][e] = hi[k][e] = 0.f;
+      }
+      store8(dst + (int64_t)(hl + k) * D, lo[k]);
+      store8(dst + (int64_t)(hl + k) * D + H, hi[k]);
     }
-    store8(dst + (int64_t)hl * D + i0, lo);
-    store8(dst + (int64_t)hl * D + H + i0, hi);
   }
 }
 
 // ----------------------------------------------------------- attention: merge
 // out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i over the row's pieces,
-// M = max m_i, in fp32.  One block of kMergeWarps warps per (row, head): each
-// warp takes every kMergeWarps-th piece, lanes the columns; the warps' sums
-// meet in shared memory.  Bound by the latency of reading the partials (L2).
+// M = max m_i, in fp32.  One block of kMergeWarps warps per (row, head): the
+// pieces go to the warps in turn, four in flight each, lanes hold the columns,
+// and the warps' sums meet in shared memory.  Bound by the latency of its chain
+// of reads (L2): the row's record -> its entry's units -> the own partials; the
+// prefix's partials are known from the arguments and are read meanwhile.
 constexpr int kMergeWarps = 4;
 
 template <int D, typename T>
@@ -190,80 +232,105 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attend_merge_kernel(const At
   const int Hq = p.Hkv * p.g;
   const int row = blockIdx.x / Hq, h = blockIdx.x % Hq, c = h / p.g, hl = h % p.g;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int2 st = p.row_info[row];
-  if (st.x < 0) return;                      // a row of no sequence: left as it was
+  const int4 info = p.row_info[row];
+  const PlanHead head = *p.head;
   const int64_t pr = (int64_t)row * p.g + hl;
-  // partial rows first + i * step: n1 of the prefix, n2 of the own tokens
-  int64_t f1 = 0, f2 = 0;
-  int n1 = 0, n2 = 0;
-  if (st.y >= 0) {
-    if (p.n_groups > 0) {
-      const int64_t total = (int64_t)p.Hkv * p.prefix_tiles, u0 = (int64_t)c * p.prefix_tiles;
-      const int64_t j0 = part_of(u0, p.n_groups, total);
-      n1 = (int)(part_of(u0 + p.prefix_tiles - 1, p.n_groups, total) - j0) + 1;
-      f1 = (c + j0) * p.rows + pr;
+
+  float m = -INFINITY, L = 0.f, acc[V] = {};   // of this warp's pieces, acc and L relative to m
+  // pieces first + i * step, i = i0, i0 + kMergeWarps, .. < n
+  auto add = [&](int64_t first, int64_t step, int i0, int n) {
+    for (int i = i0; i < n; i += 4 * kMergeWarps) {
+      float2 ml[4];
+      float x[4][V];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        const int ii = i + k * kMergeWarps;
+        if (ii < n) {
+          const int64_t r = first + ii * step;
+          ml[k] = p.ml[r];
+          const float *src = p.acc + r * D + lane * V;
+          if constexpr (V == 4) {
+            const float4 y = *reinterpret_cast<const float4 *>(src);
+            x[k][0] = y.x;
+            x[k][1] = y.y;
+            x[k][2] = y.z;
+            x[k][3] = y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2 *>(src);
+            x[k][0] = y.x;
+            x[k][1] = y.y;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e) x[k][e] = 0.f;
+        }
+      }
+      const float mn = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
+      const float mu = mn == -INFINITY ? 0.f : mn, f = exp2f(m - mu);
+      L *= f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] *= f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float w = exp2f(ml[k].x - mu);
+        L += w * ml[k].y;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] += w * x[k][e];
+      }
+      m = mn;
     }
-    const int32_t s0 = __ldg(a.batch.row_ptr + st.x);
-    const int64_t local = (int64_t)(row - s0) * p.g + hl;
+  };
+
+  int n1 = 0;
+  if (p.n_groups > 0) {
+    const int64_t total = (int64_t)p.Hkv * p.prefix_tiles, u0 = (int64_t)c * p.prefix_tiles;
+    const int64_t j0 = part_of(u0, p.n_groups, total);
+    n1 = (int)(part_of(u0 + p.prefix_tiles - 1, p.n_groups, total) - j0) + 1;
+    add((c + j0) * p.rows + pr, p.rows, warp, n1);
+  }
+  if (info.x < 0) return;                      // a row of no sequence: left as it was
+  const bool live = info.y >= 0;               // else padding: 0
+  if (live) {
+    const int64_t local = (int64_t)(row - info.z) * p.g + hl;
     const int32_t rt = (int32_t)(local / p.tile_rows);
-    const int64_t e = (int64_t)p.first_entry[st.x] + rt;
-    if (e < *p.n_entries) {
-      const int64_t total = p.units[*p.n_entries], u0 = p.units[e];
-      const int64_t tiles = (p.units[e + 1] - u0) / p.Hkv;
+    const int64_t e = head.single ? info.x : (int64_t)p.first_entry[info.x] + rt;
+    if (e < head.n_entries) {
+      const int64_t u0 = p.units[e], tiles = (p.units[e + 1] - u0) / p.Hkv;
       if (tiles > 0) {
-        const int64_t parts = own_parts(p, total);
-        const int64_t i0 = part_of(u0 + c * tiles, parts, total);
-        n2 = (int)(part_of(u0 + (c + 1) * tiles - 1, parts, total) - i0) + 1;
-        const SeqRows s = seq_rows(a.batch, st.x);
+        const int64_t parts = own_parts(p, head.units);
+        const int64_t i0 = part_of(u0 + c * tiles, parts, head.units);
+        const int n2 = (int)(part_of(u0 + (c + 1) * tiles - 1, parts, head.units) - i0) + 1;
         const int64_t tile0 = (int64_t)rt * p.tile_rows;
-        const int64_t n_rows = min((int64_t)p.tile_rows, (int64_t)s.n * p.g - tile0);
-        f2 = p.own_base + p.Hkv * ((int64_t)s0 * p.g + tile0) + c * n_rows + p.tile_rows * i0 +
-             (local - tile0);
+        const int64_t n_rows = min((int64_t)p.tile_rows, (int64_t)info.w * p.g - tile0);
+        // the warps go on in turn after the prefix's pieces
+        add(p.own_base + p.Hkv * ((int64_t)info.z * p.g + tile0) + c * n_rows +
+                p.tile_rows * i0 + (local - tile0),
+            p.tile_rows, (warp + kMergeWarps - n1 % kMergeWarps) % kMergeWarps, n2);
       }
     }
   }
-  const int n = n1 + n2;
-  auto at = [&](int i) { return i < n1 ? f1 + (int64_t)i * p.rows
-                                       : f2 + (int64_t)(i - n1) * p.tile_rows; };
-  // M over all pieces (every warp on its own)
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, p.ml[at(i)].x);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
-  const float mu = M == -INFINITY ? 0.f : M;
-  float acc[V] = {}, L = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < n; i += kMergeWarps) {
-    const int64_t r = at(i);
-    const float2 ml = p.ml[r];
-    const float w = exp2f(ml.x - mu);
-    L += w * ml.y;
-    const float *src = p.acc + r * D + lane * V;
-    if constexpr (V == 4) {
-      const float4 x = *reinterpret_cast<const float4 *>(src);
-      acc[0] += w * x.x;
-      acc[1] += w * x.y;
-      acc[2] += w * x.z;
-      acc[3] += w * x.w;
-    } else {
-      const float2 x = *reinterpret_cast<const float2 *>(src);
-      acc[0] += w * x.x;
-      acc[1] += w * x.y;
-    }
-  }
-  __shared__ float sh[kMergeWarps][D + 1];
+  __shared__ float sh[kMergeWarps][D + 2];
 #pragma unroll
   for (int e = 0; e < V; ++e) sh[warp][lane * V + e] = acc[e];
-  if (lane == 0) sh[warp][D] = L;
+  if (lane == 0) {
+    sh[warp][D] = L;
+    sh[warp][D + 1] = m;
+  }
   __syncthreads();
+  float M = sh[0][D + 1];
+#pragma unroll
+  for (int w = 1; w < kMergeWarps; ++w) M = fmaxf(M, sh[w][D + 1]);
+  const float mu = M == -INFINITY ? 0.f : M;
   for (int d = threadIdx.x; d < D; d += 32 * kMergeWarps) {
     float num = 0.f, den = 0.f;
 #pragma unroll
     for (int w = 0; w < kMergeWarps; ++w) {
-      num += sh[w][d];
-      den += sh[w][D];
+      const float f = exp2f(sh[w][D + 1] - mu);
+      num += f * sh[w][d];
+      den += f * sh[w][D];
     }
-    from_f32(den > 0.f ? num / den : 0.f,
+    from_f32(live && den > 0.f ? num / den : 0.f,
              static_cast<T *>(a.out)[((int64_t)row * Hq + h) * D + d]);
   }
 }
@@ -337,9 +404,15 @@ dbsa_status check_paged(const dbsa_config *cfg, const dbsa_paged_cache *cache,
   return DBSA_OK;
 }
 
+// Own-token ranges per CTA (they are handed out as CTAs become free).
+constexpr int kOwnWaves = 4;
+
 // Cuts the prefix into ranges.  With n_row_tiles row tiles, w waves of the
 // CTAs hold w * n_ctas / n_row_tiles ranges; the smallest w (fewest partials)
 // that leaves under 5 % of the CTAs' time idle is taken, or the best of 8.
+// (More, shorter ranges would even out the SMs' unequal speeds, but starting a
+// piece costs a CTA a few microseconds of its loads: one row tile behind 90k
+// tokens takes 69 us with one wave, 75 with two, 81 with three.)
 int prefix_groups(int n_row_tiles, int n_ctas, int64_t units) {
   int best = 1;
   double best_use = 0;
@@ -359,7 +432,7 @@ int prefix_groups(int n_row_tiles, int n_ctas, int64_t units) {
 
 struct AttendLayout {
   AttendPlan p;
-  size_t row_info, first_entry, entry, units, n_entries, q_rot, acc, ml, total;
+  size_t head, row_info, first_entry, entry, units, q_rot, acc, ml, total;
 };
 AttendLayout attend_layout(const dbsa_config *cfg, int32_t n_seqs, int32_t n_rows,
                            int64_t prefix_len) {
@@ -381,7 +454,8 @@ AttendLayout attend_layout(const dbsa_config *cfg, int32_t n_seqs, int32_t n_row
                                                (int64_t)p.Hkv * p.prefix_tiles);
   p.max_entries = n_seqs + p.rows / p.tile_rows;
   p.own_base = prefix_len == 0 ? 0 : (int64_t)(p.Hkv + p.n_groups) * p.rows;
-  p.partial_rows = p.own_base + (int64_t)p.Hkv * p.rows + (int64_t)p.tile_rows * p.n_ctas;
+  p.own_ranges = kOwnWaves * p.n_ctas;
+  p.partial_rows = p.own_base + (int64_t)p.Hkv * p.rows + (int64_t)p.tile_rows * p.own_ranges;
   const size_t elt = cfg->dtype == DBSA_F32 ? 4 : 2;
   size_t off = kStatusBytes;
   auto take = [&](size_t bytes) {
@@ -389,11 +463,11 @@ AttendLayout attend_layout(const dbsa_config *cfg, int32_t n_seqs, int32_t n_row
     off = o + bytes;
     return o;
   };
-  l.row_info = take((size_t)n_rows * sizeof(int2));
+  l.head = take(sizeof(PlanHead));
+  l.row_info = take((size_t)n_rows * sizeof(int4));
   l.first_entry = take(((size_t)n_seqs + 1) * sizeof(int32_t));
   l.entry = take((size_t)p.max_entries * sizeof(int2));
   l.units = take(((size_t)p.max_entries + 1) * sizeof(int64_t));
-  l.n_entries = take(sizeof(int32_t));
   l.q_rot = take((size_t)p.Hkv * p.rows * p.D * elt);
   l.acc = take((size_t)p.partial_rows * p.D * sizeof(float));
   l.ml = take((size_t)p.partial_rows * sizeof(float2));
@@ -545,11 +619,11 @@ dbsa_status dbsa_shared_prefix_attend(const dbsa_config *cfg, const void *q,
   if ((s = check_ws(workspace, ws_bytes, l.total)) != DBSA_OK) return s;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   a.plan = l.p;
-  a.plan.row_info = reinterpret_cast<int2 *>(ws + l.row_info);
+  a.plan.head = reinterpret_cast<PlanHead *>(ws + l.head);
+  a.plan.row_info = reinterpret_cast<int4 *>(ws + l.row_info);
   a.plan.first_entry = reinterpret_cast<int32_t *>(ws + l.first_entry);
   a.plan.entry = reinterpret_cast<int2 *>(ws + l.entry);
   a.plan.units = reinterpret_cast<int64_t *>(ws + l.units);
-  a.plan.n_entries = reinterpret_cast<int32_t *>(ws + l.n_entries);
   a.plan.q_rot = ws + l.q_rot;
   a.plan.acc = reinterpret_cast<float *>(ws + l.acc);
   a.plan.ml = reinterpret_cast<float2 *>(ws + l.ml);

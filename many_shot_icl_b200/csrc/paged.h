@@ -39,23 +39,30 @@ __device__ __forceinline__ SeqRows seq_rows(const PagedBatch &b, int s) {
   return r;
 }
 
-// (sequence, own token) of a row: sequence -1 for a row of none, a negative
-// token for padding.  A decode step has one row per sequence in order, so row
-// r is tried as sequence r before the search.
-__device__ __forceinline__ int2 row_token(const PagedBatch &b, int row) {
-  int s = min(row, b.n_seqs - 1);
-  if (!(__ldg(b.row_ptr + s) <= row && row < __ldg(b.row_ptr + s + 1))) {
+// The sequence of a row and its own token there; sequence -1 for a row of none,
+// a negative token for padding.
+struct RowToken {
+  int32_t seq, token;
+  SeqRows rows;
+};
+// A decode step has one row per sequence in order, so row r is tried as
+// sequence r (all three loads at once) before the search.
+__device__ __forceinline__ RowToken row_token(const PagedBatch &b, int row) {
+  RowToken t;
+  t.seq = min(row, b.n_seqs - 1);
+  t.rows = seq_rows(b, t.seq);
+  if (row < t.rows.row0 || row >= t.rows.row0 + t.rows.n) {
     int lo = 0, hi = b.n_seqs;   // the first sequence that ends past the row
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if (__ldg(b.row_ptr + mid + 1) > row) hi = mid; else lo = mid + 1;
     }
-    if (lo == b.n_seqs) return make_int2(-1, 0);
-    s = lo;
+    t.seq = lo < b.n_seqs ? lo : -1;
+    if (lo < b.n_seqs) t.rows = seq_rows(b, lo);
+    if (row < t.rows.row0 || row >= t.rows.row0 + t.rows.n) t.seq = -1;
   }
-  const SeqRows r = seq_rows(b, s);
-  if (row < r.row0 || row >= r.row0 + r.n) return make_int2(-1, 0);
-  return make_int2(s, r.len - r.n + (row - r.row0));
+  t.token = t.rows.len - t.rows.n + (row - t.rows.row0);
+  return t;
 }
 
 // ---- the plan of one attention call ----
@@ -68,19 +75,27 @@ __device__ __forceinline__ int2 row_token(const PagedBatch &b, int row) {
 // Prefix: the Hkv * prefix_tiles (KV head, key tile) units are cut into
 // n_groups equal ranges, and each (range, row tile) is one item; the n_row_tiles
 // items of a range are next to each other, so that they run at the same time
-// and read its keys from memory once.  Item i goes to CTA i % n_ctas.
+// and read its keys from memory once.
 // Own tokens: the units of all (sequence, row tile, KV head) entries, in that
-// order, are cut into n_ctas equal ranges (or one per unit, if those are fewer),
-// one per CTA.
+// order, are cut into own_parts() equal ranges, each an item.
+// A CTA starts with the item of its own number; the others go to whichever CTA
+// is free next (a ticket counter), since the SMs do not get equal shares of the
+// memory's bandwidth.  What an item computes does not depend on who runs it.
 //
-// Every (item or range, KV head, row tile) intersection is a piece: it leaves
-// one partial (row maximum, sum of exponentials, weighted values) per row.
+// Every (item, KV head or entry) intersection is a piece: it leaves one partial
+// (row maximum, sum of exponentials, weighted values) per row.
 // Piece (head c, range j) of the prefix keeps packed row p at partial row
 // (c + j) * rows + p: c + j is unique along the ranges, because from one piece
 // to the next either the head or the range moves on.  The piece of own-token
-// entry e in CTA i starts at own_base + first(e) + tile_rows * i, where
+// entry e in range i starts at own_base + first(e) + tile_rows * i, where
 // first(e) counts the rows of the entries before it: again unique, since a next
 // piece adds either the rows of e or tile_rows.
+struct PlanHead {
+  int64_t units;           // own-token units, all entries
+  int32_t n_entries;
+  int32_t single;          // no sequence has more than one row tile: entry s is sequence s
+  int32_t ticket;          // items taken beyond the first of each CTA
+};
 struct AttendPlan {
   int32_t g, Hkv, D;
   int32_t tile_rows, tile_keys;
@@ -89,15 +104,16 @@ struct AttendPlan {
   int32_t prefix_len, prefix_tiles;
   int32_t n_groups;        // ranges of the prefix
   int32_t n_ctas;
+  int32_t own_ranges;      // own_parts(), at most
   int32_t max_entries;     // own-token (sequence, row tile) entries, at most
   int64_t own_base;        // first own-token partial row
   int64_t partial_rows;
   // device
-  int2 *row_info;          // [n_rows]: row_token()
+  PlanHead *head;
+  int4 *row_info;          // [n_rows]: row_token(): sequence, token, its first row, its rows
   int32_t *first_entry;    // [n_seqs + 1]
   int2 *entry;             // [max_entries]: (sequence, row tile)
   int64_t *units;          // [max_entries + 1]: key-tile units (all heads) before entry e
-  int32_t *n_entries;
   void *q_rot;             // [Hkv][rows][D], cfg->dtype, rotated
   float *acc;              // [partial_rows][D], not normalised
   float2 *ml;              // [partial_rows]: (maximum in log2 units, sum)
@@ -122,86 +138,71 @@ __host__ __device__ __forceinline__ int64_t part_of(int64_t x, int64_t parts, in
   return ((x + 1) * parts - 1) / total;
 }
 
-// CTAs that share the own-token units: no range may be empty, because the
-// merge reads a partial of every CTA from a row's first to its last.
+// Ranges the own-token units are cut into: four units each at least, unless that
+// leaves CTAs without work.  No range may be empty, because the merge reads a
+// partial of every range from a row's first to its last.
 __device__ __forceinline__ int64_t own_parts(const AttendPlan &p, int64_t units) {
-  return min((int64_t)p.n_ctas, units);
+  return min((int64_t)p.own_ranges, max(units / 4, min(units, (int64_t)p.n_ctas)));
 }
 
-// Walks the pieces of one CTA in order.
+// Walks the pieces of one item in order.
 struct PieceWalk {
-  // prefix
-  int64_t item;            // next (range, row tile) item
-  int64_t pu, pend;        // units of the current item still to emit
-  int32_t pj, prt;
-  // own tokens
-  int64_t u, uend;
-  int32_t e;
+  int64_t u, uend;         // units still to emit
+  int32_t j, rt, e;        // range, row tile (prefix), entry (own tokens)
   bool own;
-  int32_t cta;
 
-  __device__ __forceinline__ void init(int32_t cta_) {
-    cta = cta_;
-    item = cta_;
-    pu = pend = 0;
-    pj = prt = 0;
-    own = false;
-    u = uend = 0;
-    e = 0;
-  }
-
-  // Whether the first piece is one of the prefix; such pieces are known from the
-  // call's arguments, without the plan in device memory.
-  __device__ __forceinline__ bool starts_shared(const AttendPlan &p) const {
+  // Items of the prefix are known from the call's arguments, without the plan
+  // in device memory.
+  static __device__ __forceinline__ bool is_shared(const AttendPlan &p, int64_t item) {
     return item < (int64_t)p.n_groups * p.n_row_tiles;
   }
 
+  // Starts an item; false if there is none of that number.
+  __device__ bool start(const AttendPlan &p, int64_t item) {
+    own = !is_shared(p, item);
+    if (!own) {
+      j = (int32_t)(item / p.n_row_tiles);
+      rt = (int32_t)(item % p.n_row_tiles);
+      const int64_t total = (int64_t)p.Hkv * p.prefix_tiles;
+      u = j * total / p.n_groups;
+      uend = (j + 1) * total / p.n_groups;
+      return true;
+    }
+    item -= (int64_t)p.n_groups * p.n_row_tiles;
+    const int64_t total = p.head->units, parts = own_parts(p, total);
+    if (item >= parts) return false;
+    j = (int32_t)item;
+    u = item * total / parts;
+    uend = (item + 1) * total / parts;
+    int lo = 0, hi = p.head->n_entries;    // the first entry that ends past u
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (p.units[mid + 1] > u) hi = mid; else lo = mid + 1;
+    }
+    e = lo;
+    return true;
+  }
+
+  // The next piece of the item; false if it has no more.
   __device__ bool next(const AttendPlan &p, const PagedBatch &b, const int32_t *prefix_pages,
                        Piece &o) {
-    if (!own) {
-      if (pu == pend) {
-        if (item < (int64_t)p.n_groups * p.n_row_tiles) {
-          pj = (int32_t)(item / p.n_row_tiles);
-          prt = (int32_t)(item % p.n_row_tiles);
-          const int64_t total = (int64_t)p.Hkv * p.prefix_tiles;
-          pu = pj * total / p.n_groups;
-          pend = (pj + 1) * total / p.n_groups;
-          item += p.n_ctas;
-        } else {
-          own = true;
-          const int32_t ne = *p.n_entries;
-          const int64_t total = p.units[ne];
-          const int64_t parts = own_parts(p, total);
-          if (cta < parts) {
-            u = cta * total / parts;
-            uend = (cta + 1) * total / parts;
-          }
-          int lo = 0, hi = ne;    // the first entry that ends past u
-          while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (p.units[mid + 1] > u) hi = mid; else lo = mid + 1;
-          }
-          e = lo;
-        }
-      }
-      if (!own) {
-        o.c = (int32_t)(pu / p.prefix_tiles);
-        o.kt0 = (int32_t)(pu % p.prefix_tiles);
-        const int64_t n = min((int64_t)(p.prefix_tiles - o.kt0), pend - pu);
-        o.kt1 = o.kt0 + (int32_t)n;
-        pu += n;
-        o.row0 = prt * p.tile_rows;
-        o.n_rows = min(p.tile_rows, p.rows - o.row0);
-        o.n_keys = p.prefix_len;
-        o.see0 = p.prefix_len;
-        o.off = 0;
-        o.shared = 1;
-        o.pages = prefix_pages;
-        o.partial = (int64_t)(o.c + pj) * p.rows + o.row0;
-        return true;
-      }
-    }
     if (u >= uend) return false;
+    if (!own) {
+      o.c = (int32_t)(u / p.prefix_tiles);
+      o.kt0 = (int32_t)(u % p.prefix_tiles);
+      const int64_t n = min((int64_t)(p.prefix_tiles - o.kt0), uend - u);
+      o.kt1 = o.kt0 + (int32_t)n;
+      u += n;
+      o.row0 = rt * p.tile_rows;
+      o.n_rows = min(p.tile_rows, p.rows - o.row0);
+      o.n_keys = p.prefix_len;
+      o.see0 = p.prefix_len;
+      o.off = 0;
+      o.shared = 1;
+      o.pages = prefix_pages;
+      o.partial = (int64_t)(o.c + j) * p.rows + o.row0;
+      return true;
+    }
     int64_t first = p.units[e], last = p.units[e + 1];
     while (last <= u) {
       ++e;
@@ -226,7 +227,7 @@ struct PieceWalk {
     o.shared = 0;
     o.pages = b.page_table + (int64_t)en.x * b.table_stride;
     o.partial = p.own_base + (int64_t)p.Hkv * o.row0 + (int64_t)o.c * o.n_rows +
-                (int64_t)p.tile_rows * cta;
+                (int64_t)p.tile_rows * j;
     return true;
   }
 };

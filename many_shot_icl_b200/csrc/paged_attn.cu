@@ -49,9 +49,18 @@ __global__ void __launch_bounds__(kSimpleThreads) attend_simple_kernel(const Att
   using T = float;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   PieceWalk walk;
-  walk.init(blockIdx.x);
   Piece pc;
-  while (walk.next(p, a.batch, a.prefix_pages, pc)) {
+  __shared__ int32_t ticket;
+  int64_t item = blockIdx.x;
+  walk.u = walk.uend = 0;
+  for (;;) {
+    while (!walk.next(p, a.batch, a.prefix_pages, pc)) {
+      if (!walk.start(p, item)) return;
+      __syncthreads();   // the ticket before has been read
+      if (tid == 0) ticket = atomicAdd(&p.head->ticket, 1);
+      __syncthreads();
+      item = (int64_t)p.n_ctas + ticket;
+    }
     __syncthreads();   // the previous piece's reads of q are done
     const T *qs = static_cast<const T *>(p.q_rot) + ((int64_t)pc.c * p.rows + pc.row0) * D;
     for (int i = tid; i < kSimpleRows * CH; i += kSimpleThreads) {
@@ -200,6 +209,7 @@ constexpr int kTcRows = 128, kTcKeys = 64;
 constexpr int kTcSoftmaxWarps = 4, kTcProducerWarp = 4, kTcQkWarp = 5, kTcPvWarp = 6;
 constexpr int kTcThreads = 224;
 constexpr int kPieceSlots = 4;
+constexpr int kQBox = 32;   // query rows per TMA box: those of a softmax warp
 constexpr uint64_t kWaitLimitNs = 4000000000ull;   // default: 4 s, far above any legitimate wait
 constexpr uint64_t kDrainLimitNs = 200000000ull;   // 0.2 s for the exit drain
 constexpr uint32_t kFull = 0xFFFFFFFFu;
@@ -344,8 +354,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     uint32_t n_pieces = 0, kn = 0, vn = 0;
     bool ok = true;
     PieceWalk walk;
-    walk.init(blockIdx.x);
-    Piece pc;
+    Piece pc = {};
+    walk.u = walk.uend = 0;
+    int64_t item = blockIdx.x;
+    int32_t ticket = -1;   // lane 0: the item after that, requested ahead
     // The producer alone waits for the kernel before (which rotated the queries
     // and built the plan of the own tokens), and only when it needs them: the
     // first tiles of a prefix piece are loaded before that.  Their pages are
@@ -358,11 +370,15 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     };
     auto load_q = [&]() {
       enter();
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bar[C::Q_FULL], C::Q_BYTES);
-#pragma unroll
-        for (int h = 0; h < C::NH; ++h)
-          tma_load_3d(sQ + h * QATOM, &tmQ, &bar[C::Q_FULL], h * 64, pc.row0, pc.c);
+      // 32 rows a box, as many as hold rows of the piece: the rows behind them
+      // keep what they held, for softmax warps that have no row of the piece
+      const int boxes = (pc.n_rows + kQBox - 1) / kQBox;
+      if (lane == 0) mbar_arrive_expect_tx(&bar[C::Q_FULL], boxes * C::NH * kQBox * 128);
+      __syncwarp();
+      if (lane < boxes * C::NH) {
+        const int b = lane / C::NH, h = lane % C::NH;
+        tma_load_3d(sQ + h * QATOM + b * kQBox * 128, &tmQ, &bar[C::Q_FULL], h * 64,
+                    pc.row0 + b * kQBox, pc.c);
       }
     };
     if (a.withhold_tiles) {
@@ -373,8 +389,13 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       while (!*abort_flag && globaltimer_ns() - t0 <= 2 * limit) __nanosleep(256);
       ok = false;
     }
-    if (!walk.starts_shared(p)) enter();
-    while (ok && walk.next(p, a.batch, a.prefix_pages, pc)) {
+    while (ok) {
+      if (!walk.next(p, a.batch, a.prefix_pages, pc)) {
+        if (n_pieces > 0 || !PieceWalk::is_shared(p, item)) enter();
+        if (n_pieces > 0) item = p.n_ctas + (int64_t)__shfl_sync(kFull, ticket, 0);
+        if (!walk.start(p, item) || !walk.next(p, a.batch, a.prefix_pages, pc)) break;
+        if (entered && lane == 0) ticket = atomicAdd(&p.head->ticket, 1);
+      }
       const uint32_t slot = n_pieces % kPieceSlots;
       if (n_pieces >= kPieceSlots &&
           !(ok = wait_warp(C::PIECE_EMPTY + slot, (n_pieces / kPieceSlots - 1) & 1)))
@@ -393,6 +414,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       for (int kt = pc.kt0; kt <= pc.kt1; ++kt) {
         if (hold_q && kt == pc.kt0 + C::NK) {   // no K slot is left to fill
           load_q();
+          if (lane == 0) ticket = atomicAdd(&p.head->ticket, 1);
           hold_q = false;
         }
         if (kt < pc.kt1) {
@@ -426,7 +448,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         page = next;
         y = next_y;
       }
-      if (hold_q) load_q();
+      if (hold_q) {
+        load_q();
+        if (lane == 0) ticket = atomicAdd(&p.head->ticket, 1);
+      }
     }
     // the end of the list
     if (ok) {
@@ -706,7 +731,7 @@ cudaError_t launch_tc(const AttendArgs &a, cudaStream_t st) {
   const cuuint64_t ks[3] = {D * 2, (cuuint64_t)a.pool.page_size * D * 2,
                             (cuuint64_t)a.pool.page_stride * 2};
   const int box = a.pool.page_size < kTcKeys ? a.pool.page_size : kTcKeys;
-  if (!encode_map(&mq, p.q_rot, 3, qd, qs, kTcRows) || !encode_map(&mk, a.pool.k, 4, kd, ks, box) ||
+  if (!encode_map(&mq, p.q_rot, 3, qd, qs, kQBox) || !encode_map(&mk, a.pool.k, 4, kd, ks, box) ||
       !encode_map(&mv, a.pool.v, 4, kd, ks, box))
     return cudaErrorInvalidValue;
   const cudaError_t e = cudaFuncSetAttribute(
