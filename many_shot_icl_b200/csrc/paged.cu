@@ -298,9 +298,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attend_merge_kernel(const At
     if (e < head.n_entries) {
       const int64_t u0 = p.units[e], tiles = (p.units[e + 1] - u0) / p.Hkv;
       if (tiles > 0) {
-        const int64_t parts = own_parts(p, head.units);
-        const int64_t i0 = part_of(u0 + c * tiles, parts, head.units);
-        const int n2 = (int)(part_of(u0 + (c + 1) * tiles - 1, parts, head.units) - i0) + 1;
+        const OwnRanges r(p, head.units);
+        const int64_t i0 = r.of(u0 + c * tiles);
+        const int n2 = (int)(r.of(u0 + (c + 1) * tiles - 1) - i0) + 1;
         const int64_t tile0 = (int64_t)rt * p.tile_rows;
         const int64_t n_rows = min((int64_t)p.tile_rows, (int64_t)info.w * p.g - tile0);
         // the warps go on in turn after the prefix's pieces
@@ -403,9 +403,6 @@ dbsa_status check_paged(const dbsa_config *cfg, const dbsa_paged_cache *cache,
   *rope = rope_tables_at(static_cast<const float *>(tables), (int32_t)n_hi, cfg->head_dim);
   return DBSA_OK;
 }
-
-// Own-token ranges per CTA (they are handed out as CTAs become free).
-constexpr int kOwnWaves = 4;
 
 // Cuts the prefix into ranges.  With n_row_tiles row tiles, w waves of the
 // CTAs hold w * n_ctas / n_row_tiles ranges; the smallest w (fewest partials)

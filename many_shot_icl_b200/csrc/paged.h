@@ -77,7 +77,7 @@ __device__ __forceinline__ RowToken row_token(const PagedBatch &b, int row) {
 // items of a range are next to each other, so that they run at the same time
 // and read its keys from memory once.
 // Own tokens: the units of all (sequence, row tile, KV head) entries, in that
-// order, are cut into own_parts() equal ranges, each an item.
+// order, are cut into ranges (OwnRanges), each an item.
 // A CTA starts with the item of its own number; the others go to whichever CTA
 // is free next (a ticket counter), since the SMs do not get equal shares of the
 // memory's bandwidth.  What an item computes does not depend on who runs it.
@@ -104,7 +104,7 @@ struct AttendPlan {
   int32_t prefix_len, prefix_tiles;
   int32_t n_groups;        // ranges of the prefix
   int32_t n_ctas;
-  int32_t own_ranges;      // own_parts(), at most
+  int32_t own_ranges;      // at most
   int32_t max_entries;     // own-token (sequence, row tile) entries, at most
   int64_t own_base;        // first own-token partial row
   int64_t partial_rows;
@@ -138,12 +138,44 @@ __host__ __device__ __forceinline__ int64_t part_of(int64_t x, int64_t parts, in
   return ((x + 1) * parts - 1) / total;
 }
 
-// Ranges the own-token units are cut into: four units each at least, unless that
-// leaves CTAs without work.  No range may be empty, because the merge reads a
-// partial of every range from a row's first to its last.
-__device__ __forceinline__ int64_t own_parts(const AttendPlan &p, int64_t units) {
-  return min((int64_t)p.own_ranges, max(units / 4, min(units, (int64_t)p.n_ctas)));
-}
+// How the own-token units are cut into ranges.  No range may be empty, because
+// the merge reads a partial of every range from a row's first to its last.
+// Long: kOwnWaves ranges per CTA, long ones first (8/16 of the units in n_ctas
+// ranges, then 4/16, 2/16, 1/16 and 1/16), so that there are few pieces and the
+// CTAs still end together.  Short: equal ranges of four units at least, unless
+// that leaves CTAs without work.
+constexpr int kOwnWaves = 5;
+struct OwnRanges {
+  int64_t units, n;        // n ranges in all
+  int32_t n_ctas;
+  bool guided;
+
+  __device__ __forceinline__ OwnRanges(const AttendPlan &p, int64_t units_)
+      : units(units_), n_ctas(p.n_ctas) {
+    guided = units >= 64 * (int64_t)n_ctas;
+    n = guided ? (int64_t)kOwnWaves * n_ctas
+               : min((int64_t)kOwnWaves * n_ctas, max(units / 4, min(units, (int64_t)n_ctas)));
+  }
+  // First unit of wave w: 16ths 0, 8, 12, 14, 15, 16.
+  __device__ __forceinline__ int64_t wave(int w) const {
+    return units * (16 - (w < 5 ? 16 >> w : 0)) / 16;
+  }
+  __device__ __forceinline__ int64_t begin(int64_t i) const {
+    if (!guided) return i * units / n;
+    const int w = (int)(i / n_ctas);
+    if (w >= kOwnWaves) return units;
+    const int64_t u = wave(w);
+    return u + i % n_ctas * (wave(w + 1) - u) / n_ctas;
+  }
+  // The range that holds unit u.
+  __device__ __forceinline__ int64_t of(int64_t u) const {
+    if (!guided) return part_of(u, n, units);
+    int w = 0;
+    while (w + 1 < kOwnWaves && wave(w + 1) <= u) ++w;
+    const int64_t u0 = wave(w);
+    return (int64_t)w * n_ctas + part_of(u - u0, n_ctas, wave(w + 1) - u0);
+  }
+};
 
 // Walks the pieces of one item in order.
 struct PieceWalk {
@@ -169,11 +201,11 @@ struct PieceWalk {
       return true;
     }
     item -= (int64_t)p.n_groups * p.n_row_tiles;
-    const int64_t total = p.head->units, parts = own_parts(p, total);
-    if (item >= parts) return false;
+    const OwnRanges r(p, p.head->units);
+    if (item >= r.n) return false;
     j = (int32_t)item;
-    u = item * total / parts;
-    uend = (item + 1) * total / parts;
+    u = r.begin(item);
+    uend = r.begin(item + 1);
     int lo = 0, hi = p.head->n_entries;    // the first entry that ends past u
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;

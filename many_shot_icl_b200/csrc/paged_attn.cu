@@ -357,7 +357,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     Piece pc = {};
     walk.u = walk.uend = 0;
     int64_t item = blockIdx.x;
-    int32_t ticket = -1;   // lane 0: the item after that, requested ahead
     // The producer alone waits for the kernel before (which rotated the queries
     // and built the plan of the own tokens), and only when it needs them: the
     // first tiles of a prefix piece are loaded before that.  Their pages are
@@ -392,9 +391,12 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     while (ok) {
       if (!walk.next(p, a.batch, a.prefix_pages, pc)) {
         if (n_pieces > 0 || !PieceWalk::is_shared(p, item)) enter();
-        if (n_pieces > 0) item = p.n_ctas + (int64_t)__shfl_sync(kFull, ticket, 0);
+        if (n_pieces > 0) {   // asked for only now, so that slow SMs take fewer
+          int32_t ticket = 0;
+          if (lane == 0) ticket = atomicAdd(&p.head->ticket, 1);
+          item = p.n_ctas + (int64_t)__shfl_sync(kFull, ticket, 0);
+        }
         if (!walk.start(p, item) || !walk.next(p, a.batch, a.prefix_pages, pc)) break;
-        if (entered && lane == 0) ticket = atomicAdd(&p.head->ticket, 1);
       }
       const uint32_t slot = n_pieces % kPieceSlots;
       if (n_pieces >= kPieceSlots &&
@@ -414,7 +416,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       for (int kt = pc.kt0; kt <= pc.kt1; ++kt) {
         if (hold_q && kt == pc.kt0 + C::NK) {   // no K slot is left to fill
           load_q();
-          if (lane == 0) ticket = atomicAdd(&p.head->ticket, 1);
           hold_q = false;
         }
         if (kt < pc.kt1) {
@@ -448,10 +449,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         page = next;
         y = next_y;
       }
-      if (hold_q) {
-        load_q();
-        if (lane == 0) ticket = atomicAdd(&p.head->ticket, 1);
-      }
+      if (hold_q) load_q();
     }
     // the end of the list
     if (ok) {
