@@ -222,7 +222,8 @@ struct Tc {
   // a tile's V is used a softmax later.
   static constexpr int NK = 2, NV = 3;
   enum Bar {
-    Q_FULL, Q_EMPTY, DRAIN_QK, DRAIN_PV, S_FULL /* [K slot, S buffer] */,
+    Q_FULL /* [piece % 2] */, Q_EMPTY = Q_FULL + 2, DRAIN_QK = Q_EMPTY + 2, DRAIN_PV,
+    S_FULL /* [K slot, S buffer] */,
     P_FULL = S_FULL + NK /* [S buffer] */, K_FULL = P_FULL + NK, V_FULL = K_FULL + NK,
     PV_DONE = V_FULL + NV /* [V slot] */, PIECE_FULL = PV_DONE + NV,
     PIECE_EMPTY = PIECE_FULL + kPieceSlots, COUNT = PIECE_EMPTY + kPieceSlots
@@ -233,6 +234,14 @@ struct Tc {
   static constexpr uint32_t NEED = TILES + 1024, SMEM = NEED > 80 * 1024 ? NEED : 80 * 1024;
   static_assert(SMEM <= 115712 && 3 * (SMEM + 1024) > 233472, "two CTAs per SM");
 };
+
+// Where the queries of a piece go: pieces of at most 64 rows take turns at the
+// halves of the Q tile, so that one's can be loaded while the other's are in
+// use (Q K^T then reads 64 rows past the piece's, whose results nobody uses).
+constexpr int kQHalf = kTcRows / 2;
+__device__ __forceinline__ int q_row0(uint32_t piece, int n_rows) {
+  return n_rows <= kQHalf && (piece & 1) ? kQHalf : 0;
+}
 
 struct PieceRec {   // what the consumers need of a Piece
   int32_t n_rows, kt0, kt1, n_keys, see0, off, shared, pad;
@@ -367,18 +376,27 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       if (!entered) asm volatile("griddepcontrol.wait;" ::: "memory");
       entered = true;
     };
-    auto load_q = [&]() {
+    int rows_before = 0;   // rows of the piece before
+    auto load_q = [&](uint32_t n) -> bool {
       enter();
+      // the place's last user: two pieces back, or one if either needs it whole
+      if (n >= 2 && !wait_warp(C::Q_EMPTY + (n & 1), (n / 2 - 1) & 1)) return false;
+      if (n >= 1 && max(rows_before, pc.n_rows) > kQHalf &&
+          !wait_warp(C::Q_EMPTY + ((n - 1) & 1), ((n - 1) / 2) & 1))
+        return false;
+      rows_before = pc.n_rows;
       // 32 rows a box, as many as hold rows of the piece: the rows behind them
       // keep what they held, for softmax warps that have no row of the piece
       const int boxes = (pc.n_rows + kQBox - 1) / kQBox;
-      if (lane == 0) mbar_arrive_expect_tx(&bar[C::Q_FULL], boxes * C::NH * kQBox * 128);
+      uint64_t *full = &bar[C::Q_FULL + (n & 1)];
+      if (lane == 0) mbar_arrive_expect_tx(full, boxes * C::NH * kQBox * 128);
       __syncwarp();
       if (lane < boxes * C::NH) {
         const int b = lane / C::NH, h = lane % C::NH;
-        tma_load_3d(sQ + h * QATOM + b * kQBox * 128, &tmQ, &bar[C::Q_FULL], h * 64,
+        tma_load_3d(sQ + h * QATOM + (q_row0(n, pc.n_rows) + b * kQBox) * 128, &tmQ, full, h * 64,
                     pc.row0 + b * kQBox, pc.c);
       }
+      return true;
     };
     if (a.withhold_tiles) {
       enter();
@@ -407,15 +425,15 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                       pc.off,    pc.shared, 0,   pc.pages,  pc.partial};
         mbar_arrive(&bar[C::PIECE_FULL + slot]);
       }
-      if (n_pieces > 0 && !(ok = wait_warp(C::Q_EMPTY, (n_pieces - 1) & 1))) break;
-      hold_q = !entered;
-      if (!hold_q) load_q();
-      ++n_pieces;
+      const uint32_t n = n_pieces++;
+      hold_q = true;
       // in the order of their use: K of a tile, then V of the tile before
       int page = -1, next = -1, y = 0, next_y = 0;
       for (int kt = pc.kt0; kt <= pc.kt1; ++kt) {
-        if (hold_q && kt == pc.kt0 + C::NK) {   // no K slot is left to fill
-          load_q();
+        // Q after the first K (whose slot is free before Q's place is), or, in
+        // the first piece, once no K slot is left to fill
+        if (hold_q && kt == pc.kt0 + (n == 0 ? C::NK : 1)) {
+          if (!(ok = load_q(n))) break;
           hold_q = false;
         }
         if (kt < pc.kt1) {
@@ -449,7 +467,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         page = next;
         y = next_y;
       }
-      if (hold_q) load_q();
+      if (ok && hold_q && (ok = load_q(n))) hold_q = false;
     }
     // the end of the list
     if (ok) {
@@ -464,7 +482,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     }
     // every load must have landed before the CTA exits
     if (lane == 0) {
-      if (n_pieces > 0) drain_wait(&bar[C::Q_FULL], (n_pieces - 1) & 1);
+      // (the last piece's Q may not have been asked for)
+      const uint32_t nq = hold_q ? n_pieces - 1 : n_pieces;
+      for (uint32_t s = 0; s < 2; ++s)
+        if (nq > s) drain_wait(&bar[C::Q_FULL + s], ((nq - 1 - s) / 2) & 1);
       for (uint32_t s = 0; s < C::NK; ++s)
         if (kn > s) drain_wait(&bar[C::K_FULL + s], ((kn - 1 - s) / C::NK) & 1);
       for (uint32_t s = 0; s < C::NV; ++s)
@@ -488,7 +509,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         const int n_keys = ring[slot].n_keys;
         if (n_rows == 0) break;
         mbar_arrive(&bar[C::PIECE_EMPTY + slot]);
-        if (qk && !(ok = wait(C::Q_FULL, n_pieces & 1))) break;
+        if (qk && !(ok = wait(C::Q_FULL + (n_pieces & 1), (n_pieces >> 1) & 1))) break;
+        const uint64_t dq = dQ + q_row0(n_pieces, n_rows) * (128 >> 4);
+        const int q_empty = C::Q_EMPTY + (n_pieces & 1);
         ++n_pieces;
         for (int kt = kt0; kt < kt1; ++kt, ++tn) {
           const uint32_t b = tn & 1, ph = (tn >> 1) & 1;
@@ -506,11 +529,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             const uint32_t d = tmem + COL_S + b * kTcKeys;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              mma_bf16_ss(d, dQ + (((kk >> 2) * QATOM + (kk & 3) * 32) >> 4),
+              mma_bf16_ss(d, dq + (((kk >> 2) * QATOM + (kk & 3) * 32) >> 4),
                           dk + (((kk >> 2) * ATOM + (kk & 3) * 32) >> 4), IDESC_QK,
                           kk > 0 ? 1u : 0u);
             mma_commit(&bar[C::S_FULL + b]);
-            if (kt == kt1 - 1) mma_commit(&bar[C::Q_EMPTY]);
+            if (kt == kt1 - 1) mma_commit(&bar[q_empty]);
           } else {
             if (!(ok = wait(C::V_FULL + vs, vph))) break;
             // P written, and O rescaled or (first tile) read out
