@@ -16,168 +16,293 @@
 namespace dbsa {
 namespace {
 
-// ------------------------------------------------------ CUDA-core kernel
-// 32 packed rows against 64 keys at a time, everything in fp32 shared memory:
-// scores with lanes on keys (warp w: rows 4w..4w+3, lane: keys lane, lane +
-// 32), outputs with lanes on columns.
-constexpr int kSimpleRows = 32, kSimpleKeys = 64, kSimpleThreads = 256;
+// ------------------------------------------------------ fp32 kernel
+// fp32 caches are attended to in fp32 on the CUDA cores: tiles of 32 packed rows
+// against 64 keys in shared memory, two CTAs of eight warps per SM.
+//
+// A warp owns four rows and one of KG groups of a tile's keys, and keeps its own
+// running maximum, sums and outputs (lanes on columns); the groups are put
+// together once, at the end of the piece.  KG follows the piece's rows (4 rows:
+// 8 groups, .., more than 16: 1), so that a decode step, whose 4 rows would give
+// one warp everything, keeps all eight busy.  For the scores a lane has two keys
+// (KG = 1), one, or the D / 2 or D / 4 dimensions of one.
+//
+// K of the next tile is fetched (cp.async) once the scores are done, V once the
+// outputs are, each while the other half of a tile is computed.  The other CTA
+// of the SM fills the waits.  Bound: FMA and shared-memory reads (four rows share
+// each K and V read) with many rows, memory with few.
+constexpr int kF32Rows = 32, kF32Keys = 64, kF32Warps = 8, kF32Threads = 32 * kF32Warps;
 
 template <int D>
-struct SimpleSmem {
-  float q[kSimpleRows][D];
-  float k[kSimpleKeys][D + 4];   // rows 4 banks apart: float4 reads by 8 lanes do not collide
-  float v[kSimpleKeys][D];
-  float p[kSimpleRows][kSimpleKeys];
-  int32_t live[kSimpleKeys];     // whether the key exists
+struct F32Smem {
+  float q[kF32Rows][D];
+  float k[kF32Keys][D + 4];   // rows 4 banks apart: float4 reads by 8 lanes do not collide
+  float v[kF32Keys][D];
+  float p[kF32Rows][kF32Keys];
+  float ml[kF32Warps][4][2];
+  int32_t ticket;
 };
 
-template <typename T>
-__device__ __forceinline__ void load8_f32(const T *src, float *dst) {
-  float f[8];
-  load8(src, f);
-  reinterpret_cast<float4 *>(dst)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4 *>(dst)[1] = make_float4(f[4], f[5], f[6], f[7]);
+// 16 bytes to shared memory, zeros where there is no source.
+__device__ __forceinline__ void copy16_async(void *dst, const void *src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm100::smem_u32(dst)),
+               "l"(src), "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All groups but the last have landed (this thread's).
+__device__ __forceinline__ void copy_wait_1() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
+// Page of the row of the tile at k0 that lane i < 8 looks up for its warp (row
+// warp + 8 i), -1 if there is none.
+__device__ __forceinline__ int row_page(const Piece &pc, const PagedPool &pool, int k0) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int key = k0 + warp + kF32Warps * lane;
+  int page = -1;
+  if (lane < kF32Keys / kF32Warps && key < pc.n_keys)
+    page = __ldg(pc.pages + (key >> pool.page_shift));
+  return page < pool.n_pages ? page : -1;
+}
+
+// One tile of keys or values: a warp copies a row at a time.
+template <int D>
+__device__ __forceinline__ void fetch_tile(float *dst, int stride, const void *pages,
+                                           const Piece &pc, const PagedPool &pool, int k0,
+                                           int page_of_lane) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int i = 0; i < kF32Keys / kF32Warps; ++i) {
+    const int r = warp + kF32Warps * i;
+    const int page = __shfl_sync(~0u, page_of_lane, i);
+    const int64_t row = (int64_t)pc.c * pool.page_size + ((k0 + r) & (pool.page_size - 1));
+    const float *src = static_cast<const float *>(pages) +
+                       (page >= 0 ? page * pool.page_stride + row * D : 0) + lane * 4;
+    if (lane * 4 < D) copy16_async(dst + r * stride + lane * 4, src, page >= 0);
+  }
+}
+
+template <int D, int KG>
+__device__ __forceinline__ void f32_piece(const AttendArgs &a, const Piece &pc, F32Smem<D> &sm) {
+  constexpr int V = D / 32, RG = kF32Warps / KG;
+  constexpr int KPW = kF32Keys / KG;                // keys of a tile per warp
+  constexpr int NK = KPW > 32 ? 2 : 1;              // keys per lane
+  constexpr int PARTS = KPW < 32 ? 32 / KPW : 1;    // lanes per key
+  const AttendPlan &p = a.plan;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rg = warp % RG, kg = warp / RG, row0 = rg * 4;
+  const int key_l = kg * KPW + lane % (KPW < 32 ? KPW : 32), part = lane / (KPW < 32 ? KPW : 32);
+
+  int page = row_page(pc, a.pool, pc.kt0 * kF32Keys);
+  fetch_tile<D>(&sm.k[0][0], D + 4, a.pool.k, pc, a.pool, pc.kt0 * kF32Keys, page);
+  copy_commit();
+  fetch_tile<D>(&sm.v[0][0], D, a.pool.v, pc, a.pool, pc.kt0 * kF32Keys, page);
+  copy_commit();
+  float m[4], l[4], o[4][V];
+  int seen[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+    seen[i] = row0 + i < pc.n_rows ? keys_seen(pc, p.g, row0 + i) : 0;
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[i][e] = 0.f;
+  }
+  for (int kt = pc.kt0; kt < pc.kt1; ++kt) {
+    const int k0 = kt * kF32Keys, next = k0 + kF32Keys;
+    const bool more = kt + 1 < pc.kt1;
+    // which of this lane's keys are there
+    bool live[NK];
+#pragma unroll
+    for (int j = 0; j < NK; ++j) {
+      const int key = k0 + key_l + 32 * j;
+      int pg = -1;
+      if (key < pc.n_keys) pg = __ldg(pc.pages + (key >> a.pool.page_shift));
+      live[j] = pg >= 0 && pg < a.pool.n_pages;
+    }
+    copy_wait_1();
+    __syncthreads();   // K is in
+    float s[4][NK] = {};
+#pragma unroll 4
+    for (int ch = 0; ch < D / 4 / PARTS; ++ch) {
+      const int d = (part + PARTS * ch) * 4;
+      float4 kk[NK];
+#pragma unroll
+      for (int j = 0; j < NK; ++j) kk[j] = *reinterpret_cast<const float4 *>(&sm.k[key_l + 32 * j][d]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 x = *reinterpret_cast<const float4 *>(&sm.q[row0 + i][d]);
+#pragma unroll
+        for (int j = 0; j < NK; ++j)
+          s[i][j] += x.x * kk[j].x + x.y * kk[j].y + x.z * kk[j].z + x.w * kk[j].w;
+      }
+    }
+    __syncthreads();   // K has been read
+    if (more) {
+      page = row_page(pc, a.pool, next);
+      fetch_tile<D>(&sm.k[0][0], D + 4, a.pool.k, pc, a.pool, next, page);
+    }
+    copy_commit();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float mt = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < NK; ++j) {
+#pragma unroll
+        for (int d = 16; d >= (PARTS > 1 ? KPW : 32); d >>= 1)
+          s[i][j] += __shfl_xor_sync(~0u, s[i][j], d);
+        s[i][j] = live[j] && k0 + key_l + 32 * j < seen[i] ? s[i][j] * a.scale_log2 : -INFINITY;
+        mt = fmaxf(mt, s[i][j]);
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) mt = fmaxf(mt, __shfl_xor_sync(~0u, mt, d));
+      const float mn = fmaxf(m[i], mt), mu = mn == -INFINITY ? 0.f : mn;
+      const float f = exp2f(m[i] - mu);
+      m[i] = mn;
+      l[i] *= f;   // summed over the lanes at the end
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[i][e] *= f;
+#pragma unroll
+      for (int j = 0; j < NK; ++j) {
+        const float w = exp2f(s[i][j] - mu);
+        if (part == 0) {
+          l[i] += w;
+          sm.p[row0 + i][key_l + 32 * j] = w;
+        }
+      }
+    }
+    copy_wait_1();
+    __syncthreads();   // V is in (and this warp's p)
+#pragma unroll 4
+    for (int k = 0; k < KPW; k += 4) {
+      float4 pr[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        pr[i] = *reinterpret_cast<const float4 *>(&sm.p[row0 + i][kg * KPW + k]);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        float v[V];
+        if constexpr (V == 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(&sm.v[kg * KPW + k + kk][lane * 4]);
+          v[0] = x.x;
+          v[1] = x.y;
+          v[2] = x.z;
+          v[3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2 *>(&sm.v[kg * KPW + k + kk][lane * 2]);
+          v[0] = x.x;
+          v[1] = x.y;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float w = kk == 0 ? pr[i].x : kk == 1 ? pr[i].y : kk == 2 ? pr[i].z : pr[i].w;
+#pragma unroll
+          for (int e = 0; e < V; ++e) o[i][e] += w * v[e];
+        }
+      }
+    }
+    __syncthreads();   // V has been read
+    if (more) fetch_tile<D>(&sm.v[0][0], D, a.pool.v, pc, a.pool, next, page);
+    copy_commit();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l[i] += __shfl_xor_sync(~0u, l[i], d);
+  if constexpr (KG > 1) {
+    // put the key groups together: group kg's outputs in the idle K tile
+    float *part_o = &sm.k[0][0];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) part_o[(warp * 4 + i) * D + lane * V + e] = o[i][e];
+      if (lane == 0) {
+        sm.ml[warp][i][0] = m[i];
+        sm.ml[warp][i][1] = l[i];
+      }
+    }
+    __syncthreads();
+    if (kg == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float M = m[i];
+#pragma unroll
+        for (int g = 1; g < KG; ++g) M = fmaxf(M, sm.ml[rg + g * RG][i][0]);
+        const float mu = M == -INFINITY ? 0.f : M;
+        float f = exp2f(m[i] - mu);
+        l[i] *= f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[i][e] *= f;
+#pragma unroll
+        for (int g = 1; g < KG; ++g) {
+          const int w = rg + g * RG;
+          f = exp2f(sm.ml[w][i][0] - mu);
+          l[i] += f * sm.ml[w][i][1];
+#pragma unroll
+          for (int e = 0; e < V; ++e) o[i][e] += f * part_o[(w * 4 + i) * D + lane * V + e];
+        }
+        m[i] = M;
+      }
+    }
+  }
+  if (kg == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = row0 + i;
+      if (r >= pc.n_rows) break;
+      float *dst = p.acc + (pc.partial + r) * D + lane * V;
+#pragma unroll
+      for (int e = 0; e < V; ++e) dst[e] = o[i][e];
+      if (lane == 0) p.ml[pc.partial + r] = make_float2(m[i], l[i]);
+    }
+  }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kSimpleThreads) attend_simple_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(kF32Threads, 2) attend_f32_kernel(const __grid_constant__ AttendArgs a) {
   pdl_enter();
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  SimpleSmem<D> &sm = *reinterpret_cast<SimpleSmem<D> *>(smem_raw);
-  constexpr int V = D / 32, CH = D / 8;
+  F32Smem<D> &sm = *reinterpret_cast<F32Smem<D> *>(smem_raw);
+  constexpr int CH = D / 4;
   const AttendPlan &p = a.plan;
-  using T = float;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   PieceWalk walk;
   Piece pc;
-  __shared__ int32_t ticket;
   int64_t item = blockIdx.x;
   walk.u = walk.uend = 0;
   for (;;) {
     while (!walk.next(p, a.batch, a.prefix_pages, pc)) {
       if (!walk.start(p, item)) return;
       __syncthreads();   // the ticket before has been read
-      if (tid == 0) ticket = atomicAdd(&p.head->ticket, 1);
+      if (tid == 0) sm.ticket = atomicAdd(&p.head->ticket, 1);
       __syncthreads();
-      item = (int64_t)p.n_ctas + ticket;
+      item = (int64_t)p.n_ctas + sm.ticket;
     }
-    __syncthreads();   // the previous piece's reads of q are done
-    const T *qs = static_cast<const T *>(p.q_rot) + ((int64_t)pc.c * p.rows + pc.row0) * D;
-    for (int i = tid; i < kSimpleRows * CH; i += kSimpleThreads) {
-      const int r = i / CH, d0 = (i % CH) * 8;
-      if (r < pc.n_rows) {
-        load8_f32(qs + (int64_t)r * D + d0, &sm.q[r][d0]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sm.q[r][d0 + e] = 0.f;
-      }
+    __syncthreads();   // the piece before is done with shared memory
+    const float *qs = static_cast<const float *>(p.q_rot) + ((int64_t)pc.c * p.rows + pc.row0) * D;
+    for (int i = tid; i < kF32Rows * CH; i += kF32Threads) {
+      const int r = i / CH, d = (i % CH) * 4;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < pc.n_rows) x = *reinterpret_cast<const float4 *>(qs + (int64_t)r * D + d);
+      *reinterpret_cast<float4 *>(&sm.q[r][d]) = x;
     }
-    float m[4], l[4], o[4][V];
-    int seen[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-      seen[i] = warp * 4 + i < pc.n_rows ? keys_seen(pc, p.g, warp * 4 + i) : 0;
-#pragma unroll
-      for (int e = 0; e < V; ++e) o[i][e] = 0.f;
-    }
-    for (int kt = pc.kt0; kt < pc.kt1; ++kt) {
-      const int k0 = kt * kSimpleKeys;
-      __syncthreads();   // the previous tile's reads are done
-      for (int i = tid; i < kSimpleKeys * CH; i += kSimpleThreads) {
-        const int r = i / CH, d0 = (i % CH) * 8, key = k0 + r;
-        int page = -1;
-        if (key < pc.n_keys) page = __ldg(pc.pages + (key >> a.pool.page_shift));
-        const bool live = page >= 0 && page < a.pool.n_pages;
-        if (live) {
-          const int64_t off =
-              page * a.pool.page_stride +
-              ((int64_t)pc.c * a.pool.page_size + (key & (a.pool.page_size - 1))) * D + d0;
-          load8_f32(static_cast<const T *>(a.pool.k) + off, &sm.k[r][d0]);
-          load8_f32(static_cast<const T *>(a.pool.v) + off, &sm.v[r][d0]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sm.k[r][d0 + e] = sm.v[r][d0 + e] = 0.f;
-        }
-        if (d0 == 0) sm.live[r] = live;
-      }
-      __syncthreads();
-      float s[4][2] = {};
-#pragma unroll 4
-      for (int d = 0; d < D; d += 4) {
-        const float4 k_0 = *reinterpret_cast<const float4 *>(&sm.k[lane][d]);
-        const float4 k_1 = *reinterpret_cast<const float4 *>(&sm.k[lane + 32][d]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 x = *reinterpret_cast<const float4 *>(&sm.q[warp * 4 + i][d]);
-          s[i][0] += x.x * k_0.x + x.y * k_0.y + x.z * k_0.z + x.w * k_0.w;
-          s[i][1] += x.x * k_1.x + x.y * k_1.y + x.z * k_1.z + x.w * k_1.w;
-        }
-      }
-      const bool live0 = sm.live[lane] != 0, live1 = sm.live[lane + 32] != 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float s0 = live0 && k0 + lane < seen[i] ? s[i][0] * a.scale_log2 : -INFINITY;
-        const float s1 = live1 && k0 + lane + 32 < seen[i] ? s[i][1] * a.scale_log2 : -INFINITY;
-        float mt = fmaxf(s0, s1);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) mt = fmaxf(mt, __shfl_xor_sync(~0u, mt, d));
-        const float mn = fmaxf(m[i], mt), mu = mn == -INFINITY ? 0.f : mn;
-        const float f = exp2f(m[i] - mu), p0 = exp2f(s0 - mu), p1 = exp2f(s1 - mu);
-        m[i] = mn;
-        l[i] = l[i] * f + p0 + p1;   // summed over the lanes at the end
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[i][e] *= f;
-        sm.p[warp * 4 + i][lane] = p0;
-        sm.p[warp * 4 + i][lane + 32] = p1;
-      }
-      __syncwarp();
-#pragma unroll 4
-      for (int k = 0; k < kSimpleKeys; k += 4) {
-        float4 pr[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          pr[i] = *reinterpret_cast<const float4 *>(&sm.p[warp * 4 + i][k]);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          float v[V];
-#pragma unroll
-          for (int e = 0; e < V; ++e) v[e] = sm.v[k + kk][lane * V + e];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float w = kk == 0 ? pr[i].x : kk == 1 ? pr[i].y : kk == 2 ? pr[i].z : pr[i].w;
-#pragma unroll
-            for (int e = 0; e < V; ++e) o[i][e] += w * v[e];
-          }
-        }
-      }
-      __syncwarp();
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float sum = l[i];
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-      const int r = warp * 4 + i;
-      if (r < pc.n_rows) {
-        float *dst = p.acc + (pc.partial + r) * D + lane * V;
-#pragma unroll
-        for (int e = 0; e < V; ++e) dst[e] = o[i][e];
-        if (lane == 0) p.ml[pc.partial + r] = make_float2(m[i], sum);
-      }
-    }
+    // (the first barrier inside orders these writes before their use)
+    if (pc.n_rows <= 4) f32_piece<D, 8>(a, pc, sm);
+    else if (pc.n_rows <= 8) f32_piece<D, 4>(a, pc, sm);
+    else if (pc.n_rows <= 16) f32_piece<D, 2>(a, pc, sm);
+    else f32_piece<D, 1>(a, pc, sm);
   }
 }
 
 template <int D>
-cudaError_t launch_simple(const AttendArgs &a, cudaStream_t st) {
+cudaError_t launch_f32(const AttendArgs &a, cudaStream_t st) {
   const cudaError_t e =
-      cudaFuncSetAttribute(attend_simple_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)sizeof(SimpleSmem<D>));
+      cudaFuncSetAttribute(attend_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)sizeof(F32Smem<D>));
   if (e != cudaSuccess) return e;
-  return pdl_launch(attend_simple_kernel<D>, dim3(a.plan.n_ctas), dim3(kSimpleThreads),
-                    sizeof(SimpleSmem<D>), st, a);
+  return pdl_launch(attend_f32_kernel<D>, dim3(a.plan.n_ctas), dim3(kF32Threads),
+                    sizeof(F32Smem<D>), st, a);
 }
 
 // ------------------------------------------------------ tensor-core kernel
@@ -767,12 +892,12 @@ cudaError_t launch_tc(const AttendArgs &a, cudaStream_t st) {
 }  // namespace
 
 AttendShape attend_shape(const dbsa_config *cfg) {
-  if (cfg->dtype == DBSA_F32) return {kSimpleRows, kSimpleKeys, 2 * 148};
+  if (cfg->dtype == DBSA_F32) return {kF32Rows, kF32Keys, 2 * 148};
   return {kTcRows, kTcKeys, 2 * 148};
 }
 
 cudaError_t launch_attend_pieces(const AttendArgs &a, int head_dim, bool f32, cudaStream_t st) {
-  if (f32) return head_dim == 128 ? launch_simple<128>(a, st) : launch_simple<64>(a, st);
+  if (f32) return head_dim == 128 ? launch_f32<128>(a, st) : launch_f32<64>(a, st);
   return head_dim == 128 ? launch_tc<128>(a, st) : launch_tc<64>(a, st);
 }
 
