@@ -24,6 +24,20 @@ __device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
   reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
+// 8 consecutive elements, bit for bit.
+template <typename T>
+struct Raw8 {
+  uint4 x[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) x[i] = reinterpret_cast<const uint4 *>(p)[i];
+  }
+  __device__ __forceinline__ void store(T *p) const {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4 *>(p)[i] = x[i];
+  }
+};
+
 // ------------------------------------------------------------------- append
 // k'[i] = k[i] cos(pos w_i) - k[i + D/2] sin(pos w_i), k'[i + D/2] = k[i +
 // D/2] cos + k[i] sin; v is copied.  Every element is read and written once:
@@ -49,25 +63,30 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs<T> a) {
   const int row = (blockIdx.x / a.pool.Hkv) * (256 / CP) + threadIdx.x / CP;
   const int i0 = (threadIdx.x % CP) * 8;
   if (row >= a.batch.n_rows) return;
+  // key and value are requested before the slot they go to is known
   const T *ks = a.k + row * a.k_row + c * a.k_head, *vs = a.v + row * a.v_row + c * a.v_head;
+  float lo[8], hi[8];
+  Raw8<T> v_lo, v_hi;
+  load8(ks + i0, lo);
+  load8(ks + H + i0, hi);
+  v_lo.load(vs + i0);
+  v_hi.load(vs + H + i0);
   const RowToken t = row_token(a.batch, row);
   if (t.seq < 0 || t.token < 0) return;
   const int page = __ldg(a.batch.page_table + (int64_t)t.seq * a.batch.table_stride +
                          (t.token >> a.pool.page_shift));
   if (page < 0 || page >= a.pool.n_pages) return;
+  float cs[8], sn[8];
+  rope_cs8(a.rope, a.pos0 + t.token, i0, H, cs, sn);
+  rotate8(lo, hi, cs, sn);
   const int64_t dst =
       page * a.pool.page_stride +
       ((int64_t)c * a.pool.page_size + (t.token & (a.pool.page_size - 1))) * D + i0;
-  float lo[8], hi[8], cs[8], sn[8];
-  load8(ks + i0, lo);
-  load8(ks + H + i0, hi);
-  rope_cs8(a.rope, a.pos0 + t.token, i0, H, cs, sn);
-  rotate8(lo, hi, cs, sn);
   T *kd = static_cast<T *>(a.pool.k) + dst, *vd = static_cast<T *>(a.pool.v) + dst;
   store8(kd, lo);
   store8(kd + H, hi);
-  copy8(vs + i0, vd);
-  copy8(vs + H + i0, vd + H);
+  v_lo.store(vd);
+  v_hi.store(vd + H);
 }
 
 // ------------------------------------------------------------ attention: plan
