@@ -236,35 +236,39 @@ __global__ void __launch_bounds__(256) attend_prep_kernel(const AttendArgs a) {
 
 // ----------------------------------------------------------- attention: merge
 // out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i over the row's pieces,
-// M = max m_i, in fp32.  One block of kMergeWarps warps per (row, head): the
-// pieces go to the warps in turn, four in flight each, lanes hold the columns,
-// and the warps' sums meet in shared memory.  Bound by the latency of its chain
-// of reads (L2): the row's record -> its entry's units -> the own partials; the
-// prefix's partials are known from the arguments and are read meanwhile.
+// M = max m_i, in fp32.  W warps per (row, head), four warps a block: the pieces
+// go to the warps in turn, four in flight each, lanes hold the columns, and the
+// warps' sums meet in shared memory.  Bound by the latency of its chain of reads
+// (L2): the row's record -> its entry's units -> the own partials; the prefix's
+// partials are known from the arguments and are read meanwhile.  W is the number
+// of pieces over four: with W = 4 throughout, 256 rows of 32 heads with 7 pieces
+// each took 34 us, four times their share of the SMs' slots.
 constexpr int kMergeWarps = 4;
 
-template <int D, typename T>
+template <int D, typename T, int W>
 __global__ void __launch_bounds__(32 * kMergeWarps) attend_merge_kernel(const AttendArgs a) {
   pdl_enter();
   constexpr int V = D / 32;   // columns per lane
   const AttendPlan &p = a.plan;
   const int Hq = p.Hkv * p.g;
-  const int row = blockIdx.x / Hq, h = blockIdx.x % Hq, c = h / p.g, hl = h % p.g;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W, sub = (threadIdx.x >> 5) / W;
+  const int64_t rh = min((int64_t)blockIdx.x * (kMergeWarps / W) + sub,
+                         (int64_t)a.batch.n_rows * Hq - 1);   // the last ones may be done twice
+  const int row = (int)(rh / Hq), h = (int)(rh % Hq), c = h / p.g, hl = h % p.g;
   const int4 info = p.row_info[row];
   const PlanHead head = *p.head;
   const int64_t pr = (int64_t)row * p.g + hl;
 
   float m = -INFINITY, L = 0.f, acc[V] = {};   // of this warp's pieces, acc and L relative to m
-  // pieces first + i * step, i = i0, i0 + kMergeWarps, .. < n
+  // pieces first + i * step, i = i0, i0 + W, .. < n
   auto add = [&](int64_t first, int64_t step, int i0, int n) {
-    for (int i = i0; i < n; i += 4 * kMergeWarps) {
+    for (int i = i0; i < n; i += 4 * W) {
       float2 ml[4];
       float x[4][V];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         ml[k] = make_float2(-INFINITY, 0.f);
-        const int ii = i + k * kMergeWarps;
+        const int ii = i + k * W;
         if (ii < n) {
           const int64_t r = first + ii * step;
           ml[k] = p.ml[r];
@@ -308,8 +312,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attend_merge_kernel(const At
     n1 = (int)(part_of(u0 + p.prefix_tiles - 1, p.n_groups, total) - j0) + 1;
     add((c + j0) * p.rows + pr, p.rows, warp, n1);
   }
-  if (info.x < 0) return;                      // a row of no sequence: left as it was
-  const bool live = info.y >= 0;               // else padding: 0
+  const bool live = info.x >= 0 && info.y >= 0;
   if (live) {
     const int64_t local = (int64_t)(row - info.z) * p.g + hl;
     const int32_t rt = (int32_t)(local / p.tile_rows);
@@ -325,11 +328,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attend_merge_kernel(const At
         // the warps go on in turn after the prefix's pieces
         add(p.own_base + p.Hkv * ((int64_t)info.z * p.g + tile0) + c * n_rows +
                 p.tile_rows * i0 + (local - tile0),
-            p.tile_rows, (warp + kMergeWarps - n1 % kMergeWarps) % kMergeWarps, n2);
+            p.tile_rows, (warp + W - n1 % W) % W, n2);
       }
     }
   }
-  __shared__ float sh[kMergeWarps][D + 2];
+  __shared__ float shared[kMergeWarps][D + 2];
+  float (*sh)[D + 2] = shared + sub * W;
 #pragma unroll
   for (int e = 0; e < V; ++e) sh[warp][lane * V + e] = acc[e];
   if (lane == 0) {
@@ -337,20 +341,21 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attend_merge_kernel(const At
     sh[warp][D + 1] = m;
   }
   __syncthreads();
+  if (info.x < 0) return;                      // a row of no sequence: left as it was
   float M = sh[0][D + 1];
 #pragma unroll
-  for (int w = 1; w < kMergeWarps; ++w) M = fmaxf(M, sh[w][D + 1]);
+  for (int w = 1; w < W; ++w) M = fmaxf(M, sh[w][D + 1]);
   const float mu = M == -INFINITY ? 0.f : M;
-  for (int d = threadIdx.x; d < D; d += 32 * kMergeWarps) {
+  T *out = static_cast<T *>(a.out) + rh * D;
+  for (int d = warp * 32 + lane; d < D; d += 32 * W) {
     float num = 0.f, den = 0.f;
 #pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
       const float f = exp2f(sh[w][D + 1] - mu);
       num += f * sh[w][d];
       den += f * sh[w][D];
     }
-    from_f32(live && den > 0.f ? num / den : 0.f,
-             static_cast<T *>(a.out)[((int64_t)row * Hq + h) * D + d]);
+    from_f32(live && den > 0.f ? num / den : 0.f, out[d]);   // 0: padding, or nothing seen
   }
 }
 
@@ -515,9 +520,17 @@ cudaError_t launch_attend_t(const AttendArgs &a, cudaStream_t st) {
     e = launch_attend_pieces(a, D, sizeof(T) == 4, st);
   }
   if (e != cudaSuccess) return e;
-  return pdl_launch(attend_merge_kernel<D, T>,
-                    dim3((unsigned)a.batch.n_rows * a.plan.Hkv * a.plan.g), dim3(32 * kMergeWarps),
-                    0, st, a);
+  // a row's pieces of the prefix: those of the ranges that its head meets
+  const int pieces = a.plan.n_groups / a.plan.Hkv + 2;
+  const int64_t rows = (int64_t)a.batch.n_rows * a.plan.Hkv * a.plan.g;
+  auto merge = [&](auto kernel, int w) {
+    const int per = kMergeWarps / w;
+    return pdl_launch(kernel, dim3((unsigned)((rows + per - 1) / per)), dim3(32 * kMergeWarps), 0,
+                      st, a);
+  };
+  if (pieces > 12) return merge(attend_merge_kernel<D, T, 4>, 4);
+  if (pieces > 8) return merge(attend_merge_kernel<D, T, 2>, 2);
+  return merge(attend_merge_kernel<D, T, 1>, 1);
 }
 
 template <int D, typename T>
