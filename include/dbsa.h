@@ -312,8 +312,8 @@ dbsa_status dbsa_gather_rope_attend_noalloc(
  * to and nothing is appended to them.
  *
  * The arrays of a batch are DEVICE arrays, read by the kernels: a call can be
- * captured into a CUDA graph and replayed after they have changed.  Their
- * contents are not checked on the host; the kernels check every index:
+ * captured into a CUDA graph (after one like it outside of capture, which loads
+ * the kernels) and replayed after they have changed.  Their contents are not checked on the host; the kernels check every index:
  *  - rows [row_ptr[s], row_ptr[s+1]) of the batch belong to sequence s; row_ptr
  *    must not decrease.  A sequence whose rows are not inside [0, n_rows] has
  *    no rows.  Rows of no sequence are ignored, and their outputs left as
@@ -375,13 +375,13 @@ dbsa_status dbsa_paged_append(const dbsa_config *cfg, const void *k, int64_t k_r
  * own sequences: row i (own token t, position prefix_len + t) attends to the
  * prefix tokens 0 .. prefix_len - 1 and to own tokens 0 .. t, whose keys and
  * values are in the cache already (dbsa_paged_append before it, on the same
- * stream).  Each prefix page is read once per 128 query rows of a KV head,
- * whatever the number of sequences.
+ * stream).  The prefix is read once per 128 query rows of a KV head (32 with
+ * DBSA_F32), whichever sequences they belong to.
  *   q            device, pre-RoPE: row r, head h at r * q_row_stride + h *
  *                head_dim (q_row_stride a multiple of 8)
  *   prefix_pages device, [ceil(prefix_len / page_size)] page ids (may be NULL
  *                when prefix_len is 0)
- *   out          device, [n_rows][Hq][D]; rows that may attend to nothing
+ *   out          device, [n_rows][Hq][D], apart from the inputs; rows that may attend to nothing
  *                (padding, or every page missing) get 0
  *   workspace    device, 256-byte aligned, ws_bytes >=
  *                dbsa_shared_prefix_workspace_size(); its contents need not be

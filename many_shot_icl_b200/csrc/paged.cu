@@ -252,9 +252,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attend_merge_kernel(const At
   const AttendPlan &p = a.plan;
   const int Hq = p.Hkv * p.g;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W, sub = (threadIdx.x >> 5) / W;
-  const int64_t rh = min((int64_t)blockIdx.x * (kMergeWarps / W) + sub,
-                         (int64_t)a.batch.n_rows * Hq - 1);   // the last ones may be done twice
-  const int row = (int)(rh / Hq), h = (int)(rh % Hq), c = h / p.g, hl = h % p.g;
+  const int rh = min((int)blockIdx.x * (kMergeWarps / W) + sub,
+                     a.batch.n_rows * Hq - 1);   // the last ones may be done twice
+  const int row = rh / Hq, h = rh % Hq, c = h / p.g, hl = h % p.g;
   const int4 info = p.row_info[row];
   const PlanHead head = *p.head;
   const int64_t pr = (int64_t)row * p.g + hl;
@@ -314,19 +314,19 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attend_merge_kernel(const At
   }
   const bool live = info.x >= 0 && info.y >= 0;
   if (live) {
-    const int64_t local = (int64_t)(row - info.z) * p.g + hl;
-    const int32_t rt = (int32_t)(local / p.tile_rows);
+    const int32_t local = (row - info.z) * p.g + hl;
+    const int32_t rt = local / p.tile_rows;
     const int64_t e = head.single ? info.x : (int64_t)p.first_entry[info.x] + rt;
     if (e < head.n_entries) {
-      const int64_t u0 = p.units[e], tiles = (p.units[e + 1] - u0) / p.Hkv;
+      const int64_t u0 = p.units[e];
+      const int32_t tiles = (int32_t)(p.units[e + 1] - u0) / p.Hkv;   // of one entry: < 2^31
       if (tiles > 0) {
         const OwnRanges r(p, head.units);
-        const int64_t i0 = r.of(u0 + c * tiles);
-        const int n2 = (int)(r.of(u0 + (c + 1) * tiles - 1) - i0) + 1;
-        const int64_t tile0 = (int64_t)rt * p.tile_rows;
-        const int64_t n_rows = min((int64_t)p.tile_rows, (int64_t)info.w * p.g - tile0);
+        const int64_t i0 = r.of(u0 + (int64_t)c * tiles);
+        const int n2 = (int)(r.of(u0 + (int64_t)(c + 1) * tiles - 1) - i0) + 1;
+        const int32_t tile0 = rt * p.tile_rows, n_rows = min(p.tile_rows, info.w * p.g - tile0);
         // the warps go on in turn after the prefix's pieces
-        add(p.own_base + p.Hkv * ((int64_t)info.z * p.g + tile0) + c * n_rows +
+        add(p.own_base + (int64_t)p.Hkv * (info.z * p.g + tile0) + c * n_rows +
                 p.tile_rows * i0 + (local - tile0),
             p.tile_rows, (warp + W - n1 % W) % W, n2);
       }
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attend_merge_kernel(const At
 #pragma unroll
   for (int w = 1; w < W; ++w) M = fmaxf(M, sh[w][D + 1]);
   const float mu = M == -INFINITY ? 0.f : M;
-  T *out = static_cast<T *>(a.out) + rh * D;
+  T *out = static_cast<T *>(a.out) + (int64_t)rh * D;
   for (int d = warp * 32 + lane; d < D; d += 32 * W) {
     float num = 0.f, den = 0.f;
 #pragma unroll
@@ -399,11 +399,14 @@ dbsa_status check_paged(const dbsa_config *cfg, const dbsa_paged_cache *cache,
     return fail(DBSA_ERR_INVALID_ARG, "page_stride too large");
   if (b->n_seqs < 1 || b->n_seqs > 65535)
     return fail(DBSA_ERR_INVALID_ARG, "n_seqs must be 1..65535 (got %d)", b->n_seqs);
-  if (b->n_rows < 1) return fail(DBSA_ERR_INVALID_ARG, "n_rows must be >= 1");
+  if (b->n_rows < 1 || b->n_rows > (1 << 30))
+    return fail(DBSA_ERR_INVALID_ARG, "n_rows must be 1..2^30 (got %d)", b->n_rows);
   if (b->table_width < 1 || b->table_stride < b->table_width)
     return fail(DBSA_ERR_INVALID_ARG, "need 1 <= table_width <= table_stride");
   const int64_t own_cap = (int64_t)b->table_width * ps;
-  if (pos0 < 0 || pos0 > (1 << 30) || own_cap > (1 << 30))
+  // (key tiles of a sequence, times the heads, are counted in 32 bits)
+  if (pos0 < 0 || pos0 > (1 << 30) || own_cap > (1 << 30) ||
+      own_cap / 16 * cfg->n_kv_heads > INT32_MAX)
     return fail(DBSA_ERR_INVALID_ARG, "sequences too long");
   if (table_positions(cfg, tables_bytes) < pos0 + own_cap)
     return fail(DBSA_ERR_INVALID_ARG, "tables cover %lld positions, the batch can reach %lld",

@@ -133,9 +133,12 @@ struct Piece {
 };
 
 // The smallest j with floor((j + 1) * total / parts) > x, i.e. the part of
-// [0, total) cut into `parts` ranges that holds x.
-__host__ __device__ __forceinline__ int64_t part_of(int64_t x, int64_t parts, int64_t total) {
-  return ((x + 1) * parts - 1) / total;
+// [0, total) cut into `parts` ranges that holds x.  (In 32 bits where it can be:
+// a 64-bit division costs ~100 instructions, and the merge kernel had ten.)
+__device__ __forceinline__ int64_t part_of(int64_t x, int64_t parts, int64_t total) {
+  const uint64_t y = (uint64_t)(x + 1) * (uint64_t)parts - 1;
+  if (((uint64_t)total * (uint64_t)parts) >> 32 == 0) return (uint32_t)y / (uint32_t)total;
+  return (int64_t)(y / (uint64_t)total);
 }
 
 // How the own-token units are cut into ranges.  No range may be empty, because

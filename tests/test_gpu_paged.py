@@ -215,6 +215,29 @@ def test_repeats_bit_for_bit_and_a_row_does_not_depend_on_the_batch_values(dtype
     assert torch.equal(b.attend(other)[0], got[0])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("long_one", [0, 70])
+def test_more_sequences_than_one_scan_of_the_plan(dtype, long_one):
+    """Over 256 sequences, with rows of one tile each, or one with several."""
+    cfg = dbsa.DbsaConfig(4, 2, 64, dtype, 5e5)
+    n_new = [i % 3 for i in range(300)]
+    lens = [n + (i * 7) % 40 for i, n in enumerate(n_new)]
+    if long_one:
+        n_new[271], lens[271] = long_one, long_one + 5
+    run_attention(cfg, 16, 150, n_new, lens, seed=30, spare_rows=1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_ranges_of_decreasing_length(dtype):
+    """Enough own tokens for ranges of several lengths per CTA."""
+    cfg = dbsa.DbsaConfig(16, 8, 64, dtype, 5e5)
+    rng = np.random.default_rng(6)
+    lens = rng.integers(3000, 6000, 48).tolist()
+    units = sum(-(-n // 64) for n in lens) * 8
+    assert units >= 64 * 296
+    run_attention(cfg, 256, 300, [1] * 48, lens, seed=31)
+
+
 def test_repeats_over_long_ragged_sequences():
     """Ragged ends in most tiles (V rows zeroed while later loads are in
     flight), several pieces per CTA: the same bits every time."""

@@ -66,6 +66,7 @@ def attend(lib, cfg=CFG, q=FAKE, q_stride=1024, prefix=FAKE, prefix_len=100, tab
     (dict(b=batch(n_seqs=0)), dbsa.ERR_INVALID_ARG),
     (dict(b=batch(n_seqs=65536)), dbsa.ERR_INVALID_ARG),
     (dict(b=batch(n_rows=0)), dbsa.ERR_INVALID_ARG),
+    (dict(b=batch(n_rows=(1 << 30) + 1)), dbsa.ERR_INVALID_ARG),
     (dict(b=batch(row_ptr=None)), dbsa.ERR_INVALID_ARG),
     (dict(b=batch(seq_lens=FAKE + 2)), dbsa.ERR_INVALID_ARG),
     (dict(b=batch(table_width=0)), dbsa.ERR_INVALID_ARG),
