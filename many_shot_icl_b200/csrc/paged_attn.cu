@@ -331,6 +331,11 @@ cudaError_t launch_f32(const AttendArgs &a, cudaStream_t st) {
 // there) get probability 0, and their rows of V are zeroed in shared memory:
 // 0 * NaN would poison the row.
 constexpr int kTcRows = 128, kTcKeys = 64;
+// Pieces of at most this many rows (a decode step's own tokens, a small batch
+// behind the prefix) run 64-row instructions: rows 0..15 lie in the same lanes of
+// the tensor memory, and half the tensor core's work, all of it on rows that do
+// not exist, is saved.  What that buys is power: the calls run at its limit.
+constexpr int kFewRows = 16;
 constexpr int kTcSoftmaxWarps = 4, kTcProducerWarp = 4, kTcQkWarp = 5, kTcPvWarp = 6;
 constexpr int kTcThreads = 224;
 constexpr int kPieceSlots = 4;
@@ -421,8 +426,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   using C = Tc<D>;
   constexpr uint32_t QATOM = kTcRows * 128;       // one 64-column atom of the Q tile
   constexpr uint32_t ATOM = kTcKeys * 128;        // ... of a K or V tile
+  // 128-row instructions, or 64-row ones
   constexpr uint32_t IDESC_QK = idesc_bf16_f32(kTcRows, kTcKeys, false);
   constexpr uint32_t IDESC_PV = idesc_bf16_f32(kTcRows, D, true);
+  constexpr uint32_t IDESC_QK_64 = idesc_bf16_f32(64, kTcKeys, false);
+  constexpr uint32_t IDESC_PV_64 = idesc_bf16_f32(64, D, true);
   constexpr uint32_t TMEM_COLS = 256, COL_S = 0, COL_O = 2 * kTcKeys;
 
   // Swizzled tiles sit on 1024-byte boundaries of shared memory: the dynamic
@@ -637,6 +645,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         if (qk && !(ok = wait(C::Q_FULL + (n_pieces & 1), (n_pieces >> 1) & 1))) break;
         const uint64_t dq = dQ + q_row0(n_pieces, n_rows) * (128 >> 4);
         const int q_empty = C::Q_EMPTY + (n_pieces & 1);
+        const uint32_t idesc = n_rows <= kFewRows ? (qk ? IDESC_QK_64 : IDESC_PV_64)
+                                                  : (qk ? IDESC_QK : IDESC_PV);
         ++n_pieces;
         for (int kt = kt0; kt < kt1; ++kt, ++tn) {
           const uint32_t b = tn & 1, ph = (tn >> 1) & 1;
@@ -655,7 +665,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               mma_bf16_ss(d, dq + (((kk >> 2) * QATOM + (kk & 3) * 32) >> 4),
-                          dk + (((kk >> 2) * ATOM + (kk & 3) * 32) >> 4), IDESC_QK,
+                          dk + (((kk >> 2) * ATOM + (kk & 3) * 32) >> 4), idesc,
                           kk > 0 ? 1u : 0u);
             mma_commit(&bar[C::S_FULL + b]);
             if (kt == kt1 - 1) mma_commit(&bar[q_empty]);
@@ -671,11 +681,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             if (valid > kTcKeys - 16) {
 #pragma unroll
               for (int kk = 0; kk < kTcKeys / 16; ++kk)
-                mma_bf16_ts(tmem + COL_O, pcol + kk * 8, dv + kk * 128, IDESC_PV,
+                mma_bf16_ts(tmem + COL_O, pcol + kk * 8, dv + kk * 128, idesc,
                             kk > 0 ? 1u : first);
             } else {
               for (int kk = 0; kk * 16 < valid; ++kk)
-                mma_bf16_ts(tmem + COL_O, pcol + kk * 8, dv + kk * 128, IDESC_PV,
+                mma_bf16_ts(tmem + COL_O, pcol + kk * 8, dv + kk * 128, idesc,
                             kk > 0 ? 1u : first);
             }
             mma_commit(&bar[C::PV_DONE + vs]);
@@ -758,7 +768,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             for (int e = 2; e < 16; e += 2)
               mt[c] = max3(mt[c], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
           }
-          const float mx = max3(mt[0], mt[1], fmaxf(mt[2], mt[3])) * sl2;
+          // (lanes without a row hold anything: they must not move the others)
+          const float mx =
+              row < pc.n_rows ? max3(mt[0], mt[1], fmaxf(mt[2], mt[3])) * sl2 : -INFINITY;
           if (kt == pc.kt0) {
             m_ref = mx;
           } else if (__any_sync(kFull, mx > m_ref + 8.f)) {
