@@ -30,7 +30,9 @@ namespace {
 // K of the next tile is fetched (cp.async) once the scores are done, V once the
 // outputs are, each while the other half of a tile is computed.  The other CTA
 // of the SM fills the waits.  Bound: FMA and shared-memory reads (four rows share
-// each K and V read) with many rows, memory with few.
+// each K and V read) with many rows, memory with few.  Measured: 1 sequence of 32
+// / 8 heads behind 90k tokens 137 us (0.82 of the copy bandwidth), 8 prompts of
+// ~30 tokens behind 4k 577 us (0.4 of the FMA rate).
 constexpr int kF32Rows = 32, kF32Keys = 64, kF32Warps = 8, kF32Threads = 32 * kF32Warps;
 
 template <int D>
@@ -326,6 +328,14 @@ cudaError_t launch_f32(const AttendArgs &a, cudaStream_t st) {
 // says that the tile's K slot is free, PV_DONE that its V slot and its S buffer
 // are.
 // O is rescaled only when a row's maximum has grown by more than 2^8.
+//
+// Measured (one layer, 32 / 8 heads of 128, prefix of 90 223 tokens): 1 sequence
+// 56 us in this kernel, 370 MB, 6.5 TB/s between its ramps; 64 sequences 105 us,
+// 0.85 PFLOP/s; 64 prompts of ~30 tokens 2.9 ms, 0.97 PFLOP/s at ~2 000 cycles
+// per 128 x 128 scores, where the tensor core alone would take 1 024 with 128-key
+// tiles and 1 536 with these (an instruction with A in shared memory takes 64
+// cycles up to N = 128).  Bound by memory with few rows, by the card's power limit
+// with many.
 //
 // Keys that do not exist (past the end of the list, or on a page that is not
 // there) get probability 0, and their rows of V are zeroed in shared memory:
