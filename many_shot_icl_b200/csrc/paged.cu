@@ -331,8 +331,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attend_merge_kernel(const At
         const int32_t tile0 = rt * p.tile_rows, n_rows = min(p.tile_rows, info.w * p.g - tile0);
         // the warps go on in turn after the prefix's pieces
         add(p.own_base + (int64_t)p.Hkv * (info.z * p.g + tile0) + c * n_rows +
-                p.tile_rows * i0 + (local - tile0),
-            p.tile_rows, (warp + W - n1 % W) % W, n2);
+                p.own_stride * i0 + (local - tile0),
+            p.own_stride, (warp + W - n1 % W) % W, n2);
       }
     }
   }
@@ -483,7 +483,8 @@ AttendLayout attend_layout(const dbsa_config *cfg, int32_t n_seqs, int32_t n_row
   p.max_entries = n_seqs + p.rows / p.tile_rows;
   p.own_base = prefix_len == 0 ? 0 : (int64_t)(p.Hkv + p.n_groups) * p.rows;
   p.own_ranges = kOwnWaves * p.n_ctas;
-  p.partial_rows = p.own_base + (int64_t)p.Hkv * p.rows + (int64_t)p.tile_rows * p.own_ranges;
+  p.own_stride = std::min(p.tile_rows, p.rows);
+  p.partial_rows = p.own_base + (int64_t)p.Hkv * p.rows + (int64_t)p.own_stride * p.own_ranges;
   const size_t elt = cfg->dtype == DBSA_F32 ? 4 : 2;
   size_t off = kStatusBytes;
   auto take = [&](size_t bytes) {

@@ -87,9 +87,9 @@ __device__ __forceinline__ RowToken row_token(const PagedBatch &b, int row) {
 // Piece (head c, range j) of the prefix keeps packed row p at partial row
 // (c + j) * rows + p: c + j is unique along the ranges, because from one piece
 // to the next either the head or the range moves on.  The piece of own-token
-// entry e in range i starts at own_base + first(e) + tile_rows * i, where
+// entry e in range i starts at own_base + first(e) + own_stride * i, where
 // first(e) counts the rows of the entries before it: again unique, since a next
-// piece adds either the rows of e or tile_rows.
+// piece adds either the rows of e or own_stride, which is no less.
 struct PlanHead {
   int64_t units;           // own-token units, all entries
   int32_t n_entries;
@@ -105,6 +105,7 @@ struct AttendPlan {
   int32_t n_groups;        // ranges of the prefix
   int32_t n_ctas;
   int32_t own_ranges;      // at most
+  int32_t own_stride;      // rows an own-token entry has at most
   int32_t max_entries;     // own-token (sequence, row tile) entries, at most
   int64_t own_base;        // first own-token partial row
   int64_t partial_rows;
@@ -262,7 +263,7 @@ struct PieceWalk {
     o.shared = 0;
     o.pages = b.page_table + (int64_t)en.x * b.table_stride;
     o.partial = p.own_base + (int64_t)p.Hkv * o.row0 + (int64_t)o.c * o.n_rows +
-                (int64_t)p.tile_rows * j;
+                (int64_t)p.own_stride * j;
     return true;
   }
 };

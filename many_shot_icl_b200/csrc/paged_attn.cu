@@ -489,6 +489,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   };
 
   if ((smem_u32(smem) & 1023u) != 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x == 0) atomicExch(a.status, DBSA_ERR_CUDA);
   } else if (warp == kTcProducerWarp) {
     // ------------------------------------------------------------ producer

@@ -193,6 +193,20 @@ def test_missing_pages_and_rows_that_see_nothing(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_pages_shared_between_tables(dtype):
+    """Two sequences forked from one, a page twice in one table, and prefix pages
+    as own pages: reads only, each as often as it is named."""
+    cfg = config("g3", dtype)
+    b = Batch(cfg, 32, 100, [1, 1, 2], [70, 70, 96], seed=20).fill()
+    b.page_table[1, :2] = b.page_table[0, :2]
+    b.page_table[2, 1] = b.page_table[2, 0]
+    b.page_table[2, 2] = b.prefix_pages[0]
+    q = b.randn(b.rows, 12, 128)
+    want, tol = b.attention(q)
+    check(b.attend(q), want, tol, dtype, "shared pages")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_strided_queries_a_wide_table_and_a_scale(dtype):
     cfg = dbsa.DbsaConfig(8, 2, 128, dtype, 1e4, softmax_scale=0.2)
     b = Batch(cfg, 32, 100, [3, 1], [70, 40], seed=11, width=3).fill()
