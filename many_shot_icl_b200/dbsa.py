@@ -353,71 +353,70 @@ def _refuse(msg: str):
     raise DbsaError(ERR_INVALID_ARG, msg)
 
 
+_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+_current_device = torch.cuda.current_device
+# (the public stream object costs 2 us, a quarter of a short call)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _run(fn, index: int, stream, *args):
     """Call fn(*args, stream) with device `index` current, on its current
-    stream unless one is given.  (The raw-stream query: the public stream
-    object costs 2 us, a quarter of a short call.)"""
-    cuda = torch.cuda
-    st = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if index == cuda.current_device():
+    stream unless one is given."""
+    st = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == _current_device():
         status = fn(*args, st)
     else:
-        with cuda.device(index):
+        with torch.cuda.device(index):
             status = fn(*args, st)
-    if status != OK:
+    if status:
         _check(status)
 
 
-def _strides(t):
-    """Row and head stride of [rows][heads][d]; 0 for a dimension of one."""
-    n, h, _ = t.shape
-    a, b, _ = t.stride()
-    return (a if n > 1 else 0), (b if h > 1 else 0)
-
-
-def _torch_dtype(cfg: DbsaConfig):
-    return torch.float32 if cfg.dtype == "f32" else torch.bfloat16
+def _config_ref(cfg: DbsaConfig):
+    """byref() of the config's struct, which is made once per config (the library
+    only reads it)."""
+    c = cfg.__dict__.get("_c")
+    if c is None:
+        c = cfg.c()
+        object.__setattr__(cfg, "_c", c)
+    return ctypes.byref(c)
 
 
 def _paged_args(cfg: DbsaConfig, k_pages, v_pages, page_table, row_ptr, seq_lens, tables, n_rows,
-                more):
-    """The cache and batch structs of a call and its device's index, after
-    checking the tensors; `more`: the call's other tensors, by name."""
-    shape, dtype = k_pages.shape, _torch_dtype(cfg)
+                index):
+    """The cache and batch structs of a call on device `index`, after checking
+    the tensors."""
+    shape, st, dtype = k_pages.shape, k_pages.stride(), _DTYPES[cfg.dtype]
     if len(shape) != 4 or v_pages.shape != shape:
         _refuse("pages must be [n_pages][n_kv_heads][page_size][head_dim], keys and values alike")
     n_pages, hkv, page_size, d = shape
     if hkv != cfg.n_kv_heads or d != cfg.head_dim:
         _refuse("pages of %d heads of %d elements; cfg has %d of %d"
                 % (hkv, d, cfg.n_kv_heads, cfg.head_dim))
-    st = k_pages.stride()
-    if (k_pages.dtype != dtype or v_pages.dtype != dtype or st[3] != 1 or st[2] != d
-            or (hkv > 1 and st[1] != page_size * d) or v_pages.stride() != st):
+    page = page_size * d
+    vst = v_pages.stride()
+    stride = st[0]
+    if n_pages == 1:
+        stride = hkv * page
+        st, vst = (stride, *st[1:]), (stride, *vst[1:])
+    if (k_pages.dtype != dtype or v_pages.dtype != dtype or st != vst or st[3] != 1 or st[2] != d
+            or (st[1] != page and hkv > 1)):
         _refuse("pages must be %s, contiguous inside a page, with one page stride" % dtype)
-    i32 = torch.int32
-    n_seqs, table = seq_lens.numel(), page_table.shape
+    n_seqs, table, pt, i32 = seq_lens.numel(), page_table.shape, page_table.stride(), torch.int32
     if (row_ptr.dtype != i32 or seq_lens.dtype != i32 or page_table.dtype != i32
             or len(table) != 2 or table[0] != n_seqs or row_ptr.numel() != n_seqs + 1):
         _refuse("row_ptr [n_seqs + 1], seq_lens [n_seqs] and page_table [n_seqs][width] must be "
                 "int32")
-    pt = page_table.stride()
+    width = table[1]
     if (not row_ptr.is_contiguous() or not seq_lens.is_contiguous()
-            or (table[1] > 1 and pt[1] != 1)):
-        _refuse("row_ptr and seq_lens must be contiguous, and the rows of page_table")
-    if not tables.is_contiguous():
-        _refuse("tables must be contiguous")
-    index = k_pages.get_device()
+            or (width > 1 and pt[1] != 1) or not tables.is_contiguous()):
+        _refuse("row_ptr, seq_lens and tables must be contiguous, and the rows of page_table")
     if index < 0 or not (index == v_pages.get_device() == page_table.get_device()
                          == row_ptr.get_device() == seq_lens.get_device() == tables.get_device()):
         _refuse("pages, page_table, row_ptr, seq_lens and tables must be on one CUDA device")
-    for name in more:
-        if more[name].get_device() != index:
-            _refuse("%s must be on the CUDA device of the pages" % name)
-    cache = PagedCache(k_pages.data_ptr(), v_pages.data_ptr(),
-                       st[0] if n_pages > 1 else hkv * page_size * d, n_pages, page_size)
-    batch = PagedBatch(n_seqs, n_rows, row_ptr.data_ptr(), seq_lens.data_ptr(),
-                       page_table.data_ptr(), table[1], pt[0] if n_seqs > 1 else max(table[1], 1))
-    return cache, batch, index
+    return (PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), stride, n_pages, page_size),
+            PagedBatch(n_seqs, n_rows, row_ptr.data_ptr(), seq_lens.data_ptr(),
+                       page_table.data_ptr(), width, pt[0] if n_seqs > 1 else width))
 
 
 def rope_tables_size(cfg: DbsaConfig, n_pos: int) -> int:
@@ -440,19 +439,23 @@ def paged_append(cfg: DbsaConfig, k, v, k_pages, v_pages, page_table, row_ptr, s
     """Append the rows k, v [n_rows][n_kv_heads][head_dim] (any row and head
     stride) of a batch to their sequences' pages, keys rotated at pos0 + their
     index in the sequence (see dbsa_paged_append)."""
-    shape = k.shape
-    cache, batch, index = _paged_args(cfg, k_pages, v_pages, page_table, row_ptr, seq_lens, tables,
-                                      shape[0], {"k": k, "v": v})
-    dtype = _torch_dtype(cfg)
-    if (k.dtype != dtype or v.dtype != dtype or shape != v.shape or len(shape) != 3
-            or shape[1] != cfg.n_kv_heads or shape[2] != cfg.head_dim or k.stride(2) != 1
-            or v.stride(2) != 1):
+    if _lib is None:
+        load()
+    shape, ks, vs, index = k.shape, k.stride(), v.stride(), k_pages.get_device()
+    cache, batch = _paged_args(cfg, k_pages, v_pages, page_table, row_ptr, seq_lens, tables,
+                               shape[0], index)
+    dtype = _DTYPES[cfg.dtype]
+    if (k.dtype != dtype or v.dtype != dtype or len(shape) != 3 or v.shape != shape
+            or shape[1] != cfg.n_kv_heads or shape[2] != cfg.head_dim or ks[2] != 1 or vs[2] != 1):
         _refuse("k and v must be %s [n_rows][n_kv_heads][head_dim] with contiguous elements"
                 % dtype)
-    c = cfg.c()
-    _run(load().dbsa_paged_append, index, stream, ctypes.byref(c), k.data_ptr(), *_strides(k),
-         v.data_ptr(), *_strides(v), ctypes.byref(cache), ctypes.byref(batch), pos0,
-         tables.data_ptr(), tables.numel() * tables.element_size())
+    if k.get_device() != index or v.get_device() != index:
+        _refuse("k and v must be on the CUDA device of the pages")
+    if (ks[0] | ks[1] | vs[0] | vs[1]) & 7:   # the stride of a dimension of one means nothing
+        ks, vs = ([x if n > 1 else 0 for x, n in zip(t, shape)] for t in (ks, vs))
+    _run(_lib.dbsa_paged_append, index, stream, _config_ref(cfg), k.data_ptr(), ks[0], ks[1],
+         v.data_ptr(), vs[0], vs[1], ctypes.byref(cache), ctypes.byref(batch), pos0,
+         tables.data_ptr(), tables.nbytes)
 
 
 def shared_prefix_workspace_size(cfg: DbsaConfig, n_seqs: int, n_rows: int,
@@ -468,30 +471,30 @@ def shared_prefix_attend(cfg: DbsaConfig, q, k_pages, v_pages, prefix_pages, pre
     over a shared prefix and, causally, each row's own sequence, into out of
     the same shape, contiguous (see dbsa_shared_prefix_attend).  prefix_pages
     may be None when prefix_len is 0."""
-    shape = q.shape
-    more = {"q": q, "out": out, "workspace": workspace}
-    if prefix_len > 0:
-        if prefix_pages is None:
-            _refuse("prefix_pages is None")
-        more["prefix_pages"] = prefix_pages
-    cache, batch, index = _paged_args(cfg, k_pages, v_pages, page_table, row_ptr, seq_lens, tables,
-                                      shape[0], more)
-    dtype = _torch_dtype(cfg)
-    d = cfg.head_dim
-    st = q.stride()
+    if _lib is None:
+        load()
+    shape, st, index, d = q.shape, q.stride(), k_pages.get_device(), cfg.head_dim
+    cache, batch = _paged_args(cfg, k_pages, v_pages, page_table, row_ptr, seq_lens, tables,
+                               shape[0], index)
+    dtype = _DTYPES[cfg.dtype]
     if (q.dtype != dtype or len(shape) != 3 or shape[1] != cfg.n_q_heads or shape[2] != d
-            or st[2] != 1 or (shape[1] > 1 and st[1] != d)):
+            or st[2] != 1 or (st[1] != d and shape[1] > 1)):
         _refuse("q must be %s [n_rows][n_q_heads][head_dim], each row contiguous" % dtype)
     if out.dtype != dtype or out.shape != shape or not out.is_contiguous():
         _refuse("out must be %s, contiguous, of q's shape" % dtype)
     if not workspace.is_contiguous():
         _refuse("workspace must be contiguous")
+    if not (index == q.get_device() == out.get_device() == workspace.get_device()):
+        _refuse("q, out and workspace must be on the CUDA device of the pages")
+    prefix = None
     if prefix_len > 0:
-        if (prefix_pages.dtype != torch.int32 or not prefix_pages.is_contiguous()
+        if (prefix_pages is None or prefix_pages.dtype != torch.int32
+                or not prefix_pages.is_contiguous() or prefix_pages.get_device() != index
                 or prefix_pages.numel() * cache.page_size < prefix_len):
-            _refuse("prefix_pages must be contiguous int32, one entry per page of the prefix")
-    c = cfg.c()
-    _run(load().dbsa_shared_prefix_attend, index, stream, ctypes.byref(c), q.data_ptr(),
-         st[0] if shape[0] > 1 else 0, ctypes.byref(cache), _dp(prefix_pages), prefix_len,
-         ctypes.byref(batch), tables.data_ptr(), tables.numel() * tables.element_size(),
-         out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+            _refuse("prefix_pages must be contiguous int32 on the CUDA device of the pages, one "
+                    "entry per page of the prefix")
+        prefix = prefix_pages.data_ptr()
+    _run(_lib.dbsa_shared_prefix_attend, index, stream, _config_ref(cfg), q.data_ptr(),
+         st[0] if shape[0] > 1 else 0, ctypes.byref(cache), prefix, prefix_len,
+         ctypes.byref(batch), tables.data_ptr(), tables.nbytes, out.data_ptr(),
+         workspace.data_ptr(), workspace.nbytes)
