@@ -435,26 +435,29 @@ dbsa_status check_paged(const dbsa_config *cfg, const dbsa_paged_cache *cache,
   return DBSA_OK;
 }
 
-// Cuts the prefix into ranges.  With n_row_tiles row tiles, w waves of the
-// CTAs hold w * n_ctas / n_row_tiles ranges; the smallest w (fewest partials)
-// that leaves under 5 % of the CTAs' time idle is taken, or the best of 8.
-// (More, shorter ranges would even out the SMs' unequal speeds, but starting a
-// piece costs a CTA a few microseconds of its loads: one row tile behind 90k
-// tokens takes 69 us with one wave, 75 with two, 81 with three.)
-int prefix_groups(int n_row_tiles, int n_ctas, int64_t units) {
+// How many ranges the prefix is cut into: the number for which waves of the CTAs
+// x (key tiles of an item + a piece's own cost) + the partials' traffic is least,
+// with measured costs: a key tile takes a CTA ~1.4 us (32 KB at its share of the
+// memory, or 128 rows' arithmetic at the power limit), starting and ending a piece
+// ~4 us, writing and merging the partials of a row ~0.17 ns x D / 128 of all CTAs'
+// time.  (More, shorter ranges would also even out the SMs' unequal speeds, but
+// behind 90k tokens one row tile takes 69 us with one wave, 75 with two.)
+int prefix_groups(int rows, int n_row_tiles, int n_ctas, int Hkv, int D, int64_t units) {
+  constexpr double kTile = 1.4, kPiece = 4.0, kRow = 0.17e-3;   // us
   int best = 1;
-  double best_use = 0;
-  for (int w = 1; w <= 8; ++w) {
-    const int64_t groups =
-        std::min<int64_t>(std::max<int64_t>((int64_t)w * n_ctas / n_row_tiles, 1), units);
-    const int64_t items = groups * n_row_tiles;
-    const double use = (double)items / (double)((items + n_ctas - 1) / n_ctas * n_ctas);
-    if (use > best_use + 1e-9) {
+  double best_time = 0;
+  auto consider = [&](int64_t groups) {
+    groups = std::min<int64_t>(std::max<int64_t>(groups, 1), units);
+    const double waves = (double)((groups * n_row_tiles + n_ctas - 1) / n_ctas);
+    const double time = waves * ((double)units / (double)groups * kTile + kPiece) +
+                        kRow * (double)(groups + Hkv) * rows * D / 128;
+    if (best_time == 0 || time < 0.99 * best_time) {
       best = (int)groups;
-      best_use = use;
+      best_time = time;
     }
-    if (best_use > 0.95 || groups == units) break;
-  }
+  };
+  for (int cut = 64; cut > 1; cut /= 2) consider(n_ctas / n_row_tiles / cut);   // part of a wave
+  for (int64_t w = 1; w <= 8; ++w) consider(w * n_ctas / n_row_tiles);
   return best;
 }
 
@@ -478,7 +481,7 @@ AttendLayout attend_layout(const dbsa_config *cfg, int32_t n_seqs, int32_t n_row
   p.prefix_len = (int32_t)prefix_len;
   p.prefix_tiles = (int32_t)((prefix_len + p.tile_keys - 1) / p.tile_keys);
   p.n_groups = prefix_len == 0 ? 0
-                               : prefix_groups(p.n_row_tiles, p.n_ctas,
+                               : prefix_groups(p.rows, p.n_row_tiles, p.n_ctas, p.Hkv, p.D,
                                                (int64_t)p.Hkv * p.prefix_tiles);
   p.max_entries = n_seqs + p.rows / p.tile_rows;
   p.own_base = prefix_len == 0 ? 0 : (int64_t)(p.Hkv + p.n_groups) * p.rows;
