@@ -142,11 +142,10 @@ __device__ void build_plan(const AttendPlan &p, const PagedBatch &b) {
       int64_t n = 0;
       if (e < b.n_seqs) {
         if (b.n_seqs > 256) s = seq_rows(b, e);
-        p.entry[e] = make_int2(e, 0);
         if (s.n > 0) n = tile_units(p, s, 0);
       }
       const int64_t first = units + block_scan(n, &total);
-      if (e < b.n_seqs) p.units[e] = first;
+      if (e < b.n_seqs) p.entry[e] = {e, 0, s.row0, s.n, first, s.len, 0};
       units += total;
     }
     at = b.n_seqs;
@@ -166,23 +165,25 @@ __device__ void build_plan(const AttendPlan &p, const PagedBatch &b) {
     for (int e0 = 0; e0 < at; e0 += 256) {
       const int e = e0 + tid;
       int64_t n = 0;
+      int32_t seq = 0, rt = 0;
       if (e < at) {
         int lo = 0, hi = b.n_seqs;   // the first sequence whose entries end past e
         while (lo < hi) {
           const int mid = (lo + hi) >> 1;
           if (p.first_entry[mid + 1] > e) hi = mid; else lo = mid + 1;
         }
-        const int rt = e - p.first_entry[lo];
-        p.entry[e] = make_int2(lo, rt);
-        n = tile_units(p, seq_rows(b, lo), rt);
+        seq = lo;
+        rt = e - p.first_entry[lo];
+        s = seq_rows(b, lo);
+        n = tile_units(p, s, rt);
       }
       const int64_t first = units + block_scan(n, &total);
-      if (e < at) p.units[e] = first;
+      if (e < at) p.entry[e] = {seq, rt, s.row0, s.n, first, s.len, 0};
       units += total;
     }
   }
   if (tid == 0) {
-    p.units[at] = units;
+    p.entry[at].units = units;
     *p.head = {units, (int32_t)at, single, 0};
   }
 }
@@ -240,13 +241,15 @@ __global__ void __launch_bounds__(256) attend_prep_kernel(const AttendArgs a) {
 
 // ----------------------------------------------------------- attention: merge
 // out = sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i over the row's pieces,
-// M = max m_i, in fp32.  W warps per (row, head), four warps a block: the pieces
-// go to the warps in turn, four in flight each, lanes hold the columns, and the
-// warps' sums meet in shared memory.  Bound by the latency of its chain of reads
-// (L2): the row's record -> its entry's units -> the own partials; the prefix's
-// partials are known from the arguments and are read meanwhile.  W is the number
-// of pieces over four: with W = 4 throughout, 256 rows of 32 heads with 7 pieces
-// each took 34 us, four times their share of the SMs' slots.
+// M = max m_i, in fp32.  Many pieces (W > 1): W warps per (row, head), which take
+// the pieces in turn and meet in shared memory.  Few (W = 1): a warp per (row, KV
+// head) does its g heads one after the other, the record of the row read once.
+// Four warps a block, four pieces in flight per warp, lanes hold the columns.
+// Bound by the latency of its chain of reads (L2): the row's record -> its entry
+// -> the own partials; the prefix's partials are known from the arguments and are
+// read meanwhile.  W is the number of pieces over four: with W = 4 throughout, 256
+// rows of 32 heads with 7 pieces each took 34 us; a warp per (row, head) took 50 us
+// for 2 000 rows of 32 heads with 2 or 3.
 constexpr int kMergeWarps = 4;
 
 template <int D, typename T, int W>
@@ -254,16 +257,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attend_merge_kernel(const At
   pdl_enter();
   constexpr int V = D / 32;   // columns per lane
   const AttendPlan &p = a.plan;
-  const int Hq = p.Hkv * p.g;
+  const int heads = W == 1 ? p.Hkv : p.Hkv * p.g;   // units of work per row
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W, sub = (threadIdx.x >> 5) / W;
   const int rh = min((int)blockIdx.x * (kMergeWarps / W) + sub,
-                     a.batch.n_rows * Hq - 1);   // the last ones may be done twice
-  const int row = rh / Hq, h = rh % Hq, c = h / p.g, hl = h % p.g;
+                     a.batch.n_rows * heads - 1);   // the last ones may be done twice
+  const int row = rh / heads, c = W == 1 ? rh % heads : rh % heads / p.g;
+  const int hl0 = W == 1 ? 0 : rh % heads % p.g, hl1 = W == 1 ? p.g : hl0 + 1;
   const int4 info = p.row_info[row];
   const PlanHead head = *p.head;
-  const int64_t pr = (int64_t)row * p.g + hl;
 
-  float m = -INFINITY, L = 0.f, acc[V] = {};   // of this warp's pieces, acc and L relative to m
+  float m, L, acc[V];   // of this warp's pieces of a head, acc and L relative to m
   // pieces first + i * step, i = i0, i0 + W, .. < n
   auto add = [&](int64_t first, int64_t step, int i0, int n) {
     for (int i = i0; i < n; i += 4 * W) {
@@ -309,57 +312,98 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attend_merge_kernel(const At
     }
   };
 
+  // pieces of the prefix: n1, of local head hl from f1 + hl
   int n1 = 0;
+  int64_t f1 = 0;
   if (p.n_groups > 0) {
     const int64_t total = (int64_t)p.Hkv * p.prefix_tiles, u0 = (int64_t)c * p.prefix_tiles;
     const int64_t j0 = part_of(u0, p.n_groups, total);
     n1 = (int)(part_of(u0 + p.prefix_tiles - 1, p.n_groups, total) - j0) + 1;
-    add((c + j0) * p.rows + pr, p.rows, warp, n1);
+    f1 = (c + j0) * p.rows + (int64_t)row * p.g;
   }
+  // of the own tokens, in the row tile of local row `local`: n2 from f2
   const bool live = info.x >= 0 && info.y >= 0;
-  if (live) {
-    const int32_t local = (row - info.z) * p.g + hl;
-    const int32_t rt = local / p.tile_rows;
-    const int64_t e = head.single ? info.x : (int64_t)p.first_entry[info.x] + rt;
-    if (e < head.n_entries) {
-      const int64_t u0 = p.units[e];
-      const int32_t tiles = (int32_t)(p.units[e + 1] - u0) / p.Hkv;   // of one entry: < 2^31
-      if (tiles > 0) {
-        const OwnRanges r(p, head.units);
-        const int64_t i0 = r.of(u0 + (int64_t)c * tiles);
-        const int n2 = (int)(r.of(u0 + (int64_t)(c + 1) * tiles - 1) - i0) + 1;
-        const int32_t tile0 = rt * p.tile_rows, n_rows = min(p.tile_rows, info.w * p.g - tile0);
-        // the warps go on in turn after the prefix's pieces
-        add(p.own_base + (int64_t)p.Hkv * (info.z * p.g + tile0) + c * n_rows +
-                p.own_stride * i0 + (local - tile0),
-            p.own_stride, (warp + W - n1 % W) % W, n2);
+  int rt_of = -1, n2 = 0;
+  int64_t f2 = 0;
+  auto own = [&](int hl) {
+    const int32_t local = (row - info.z) * p.g + hl, rt = local / p.tile_rows;
+    if (rt != rt_of) {
+      rt_of = rt;
+      n2 = 0;
+      const int64_t e = head.single ? info.x : (int64_t)p.first_entry[info.x] + rt;
+      if (e < head.n_entries) {
+        const int64_t u0 = p.entry[e].units;
+        const int32_t tiles = (int32_t)(p.entry[e + 1].units - u0) / p.Hkv;
+        if (tiles > 0) {
+          const OwnRanges r(p, head.units);
+          const int64_t i0 = r.of(u0 + (int64_t)c * tiles);
+          n2 = (int)(r.of(u0 + (int64_t)(c + 1) * tiles - 1) - i0) + 1;
+          const int32_t tile0 = rt * p.tile_rows, n_rows = min(p.tile_rows, info.w * p.g - tile0);
+          f2 = p.own_base + (int64_t)p.Hkv * (info.z * p.g + tile0) + c * n_rows +
+               p.own_stride * i0 - tile0;   // + local: the row
+        }
       }
     }
-  }
-  __shared__ float shared[kMergeWarps][D + 2];
-  float (*sh)[D + 2] = shared + sub * W;
+    if (n2 > 0)   // the warps go on in turn after the prefix's pieces
+      add(f2 + local, p.own_stride, (warp + W - n1 % W) % W, n2);
+  };
+
+  if constexpr (W == 1) {
+    if (info.x < 0) return;   // a row of no sequence: left as it was
+    T *out = static_cast<T *>(a.out) + ((int64_t)row * p.Hkv + c) * p.g * D + lane * V;
+#pragma unroll 2
+    for (int hl = hl0; hl < hl1; ++hl) {
+      m = -INFINITY;
+      L = 0.f;
 #pragma unroll
-  for (int e = 0; e < V; ++e) sh[warp][lane * V + e] = acc[e];
-  if (lane == 0) {
-    sh[warp][D] = L;
-    sh[warp][D + 1] = m;
-  }
-  __syncthreads();
-  if (info.x < 0) return;                      // a row of no sequence: left as it was
-  float M = sh[0][D + 1];
+      for (int e = 0; e < V; ++e) acc[e] = 0.f;
+      if (live) {
+        add(f1 + hl, p.rows, 0, n1);
+        own(hl);
+      }
+      const float inv = L > 0.f ? 1.f / L : 0.f;   // 0: padding, or nothing seen
+      T y[V];
 #pragma unroll
-  for (int w = 1; w < W; ++w) M = fmaxf(M, sh[w][D + 1]);
-  const float mu = M == -INFINITY ? 0.f : M;
-  T *out = static_cast<T *>(a.out) + (int64_t)rh * D;
-  for (int d = warp * 32 + lane; d < D; d += 32 * W) {
-    float num = 0.f, den = 0.f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const float f = exp2f(sh[w][D + 1] - mu);
-      num += f * sh[w][d];
-      den += f * sh[w][D];
+      for (int e = 0; e < V; ++e) from_f32(acc[e] * inv, y[e]);
+      if constexpr (sizeof(y) == 16)
+        *reinterpret_cast<uint4 *>(out + hl * D) = *reinterpret_cast<uint4 *>(y);
+      else if constexpr (sizeof(y) == 8)
+        *reinterpret_cast<uint2 *>(out + hl * D) = *reinterpret_cast<uint2 *>(y);
+      else
+        *reinterpret_cast<uint32_t *>(out + hl * D) = *reinterpret_cast<uint32_t *>(y);
     }
-    from_f32(live && den > 0.f ? num / den : 0.f, out[d]);   // 0: padding, or nothing seen
+  } else {
+    __shared__ float shared[kMergeWarps][D + 2];
+    float (*sh)[D + 2] = shared + sub * W;
+    m = -INFINITY;
+    L = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+    add(f1 + hl0, p.rows, warp, n1);
+    if (live) own(hl0);
+#pragma unroll
+    for (int e = 0; e < V; ++e) sh[warp][lane * V + e] = acc[e];
+    if (lane == 0) {
+      sh[warp][D] = L;
+      sh[warp][D + 1] = m;
+    }
+    __syncthreads();
+    if (info.x < 0) return;
+    float M = sh[0][D + 1];
+#pragma unroll
+    for (int w = 1; w < W; ++w) M = fmaxf(M, sh[w][D + 1]);
+    const float mu = M == -INFINITY ? 0.f : M;
+    T *out = static_cast<T *>(a.out) + (int64_t)rh * D;
+    for (int d = warp * 32 + lane; d < D; d += 32 * W) {
+      float num = 0.f, den = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float f = exp2f(sh[w][D + 1] - mu);
+        num += f * sh[w][d];
+        den += f * sh[w][D];
+      }
+      from_f32(live && den > 0.f ? num / den : 0.f, out[d]);
+    }
   }
 }
 
@@ -463,7 +507,7 @@ int prefix_groups(int rows, int n_row_tiles, int n_ctas, int Hkv, int D, int64_t
 
 struct AttendLayout {
   AttendPlan p;
-  size_t head, row_info, first_entry, entry, units, q_rot, acc, ml, total;
+  size_t head, row_info, first_entry, entry, q_rot, acc, ml, total;
 };
 AttendLayout attend_layout(const dbsa_config *cfg, int32_t n_seqs, int32_t n_rows,
                            int64_t prefix_len) {
@@ -498,8 +542,7 @@ AttendLayout attend_layout(const dbsa_config *cfg, int32_t n_seqs, int32_t n_row
   l.head = take(sizeof(PlanHead));
   l.row_info = take((size_t)n_rows * sizeof(int4));
   l.first_entry = take(((size_t)n_seqs + 1) * sizeof(int32_t));
-  l.entry = take((size_t)p.max_entries * sizeof(int2));
-  l.units = take(((size_t)p.max_entries + 1) * sizeof(int64_t));
+  l.entry = take(((size_t)p.max_entries + 1) * sizeof(Entry));
   l.q_rot = take((size_t)p.Hkv * p.rows * p.D * elt);
   l.acc = take((size_t)p.partial_rows * p.D * sizeof(float));
   l.ml = take((size_t)p.partial_rows * sizeof(float2));
@@ -533,8 +576,8 @@ cudaError_t launch_attend_t(const AttendArgs &a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   // a row's pieces of the prefix: those of the ranges that its head meets
   const int pieces = a.plan.n_groups / a.plan.Hkv + 2;
-  const int64_t rows = (int64_t)a.batch.n_rows * a.plan.Hkv * a.plan.g;
   auto merge = [&](auto kernel, int w) {
+    const int64_t rows = (int64_t)a.batch.n_rows * a.plan.Hkv * (w == 1 ? 1 : a.plan.g);
     const int per = kMergeWarps / w;
     return pdl_launch(kernel, dim3((unsigned)((rows + per - 1) / per)), dim3(32 * kMergeWarps), 0,
                       st, a);
@@ -662,8 +705,7 @@ dbsa_status dbsa_shared_prefix_attend(const dbsa_config *cfg, const void *q,
   a.plan.head = reinterpret_cast<PlanHead *>(ws + l.head);
   a.plan.row_info = reinterpret_cast<int4 *>(ws + l.row_info);
   a.plan.first_entry = reinterpret_cast<int32_t *>(ws + l.first_entry);
-  a.plan.entry = reinterpret_cast<int2 *>(ws + l.entry);
-  a.plan.units = reinterpret_cast<int64_t *>(ws + l.units);
+  a.plan.entry = reinterpret_cast<Entry *>(ws + l.entry);
   a.plan.q_rot = ws + l.q_rot;
   a.plan.acc = reinterpret_cast<float *>(ws + l.acc);
   a.plan.ml = reinterpret_cast<float2 *>(ws + l.ml);

@@ -96,6 +96,14 @@ struct PlanHead {
   int32_t single;          // no sequence has more than one row tile: entry s is sequence s
   int32_t ticket;          // items taken beyond the first of each CTA
 };
+// One (sequence, row tile) of the own tokens, and the key-tile units (all heads)
+// before it; one more record at the end holds their sum.  All that a piece needs,
+// in one read.
+struct alignas(16) Entry {
+  int32_t seq, rt, row0, n;   // row0, n, len: of the sequence (SeqRows)
+  int64_t units;
+  int32_t len, pad;
+};
 struct AttendPlan {
   int32_t g, Hkv, D;
   int32_t tile_rows, tile_keys;
@@ -113,8 +121,7 @@ struct AttendPlan {
   PlanHead *head;
   int4 *row_info;          // [n_rows]: row_token(): sequence, token, its first row, its rows
   int32_t *first_entry;    // [n_seqs + 1]
-  int2 *entry;             // [max_entries]: (sequence, row tile)
-  int64_t *units;          // [max_entries + 1]: key-tile units (all heads) before entry e
+  Entry *entry;            // [max_entries + 1]
   void *q_rot;             // [Hkv][rows][D], cfg->dtype, rotated
   float *acc;              // [partial_rows][D], not normalised
   float2 *ml;              // [partial_rows]: (maximum in log2 units, sum)
@@ -193,7 +200,7 @@ struct PieceWalk {
     return item < (int64_t)p.n_groups * p.n_row_tiles;
   }
 
-  // Starts an item; false if there is none of that number.
+  // Starts an item; false if there is none of that number.  Run by whole warps.
   __device__ bool start(const AttendPlan &p, int64_t item) {
     own = !is_shared(p, item);
     if (!own) {
@@ -210,10 +217,15 @@ struct PieceWalk {
     j = (int32_t)item;
     u = r.begin(item);
     uend = r.begin(item + 1);
-    int lo = 0, hi = p.head->n_entries;    // the first entry that ends past u
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (p.units[mid + 1] > u) hi = mid; else lo = mid + 1;
+    // the first entry that ends past u, 32 tries at a time
+    int lo = 0, hi = p.head->n_entries;
+    for (;;) {
+      const int step = (hi - lo + 31) / 32;
+      const int at = min(lo + ((int)(threadIdx.x & 31) + 1) * step, hi);
+      const int first = __ffs(__ballot_sync(~0u, p.entry[at].units > u)) - 1;
+      lo += first * step;
+      if (step == 1) break;
+      hi = min(lo + step, hi);
     }
     e = lo;
     return true;
@@ -239,29 +251,26 @@ struct PieceWalk {
       o.partial = (int64_t)(o.c + j) * p.rows + o.row0;
       return true;
     }
-    int64_t first = p.units[e], last = p.units[e + 1];
+    Entry en = p.entry[e];
+    int64_t last = p.entry[e + 1].units;
     while (last <= u) {
-      ++e;
-      first = last;
-      last = p.units[e + 1];
+      en = p.entry[++e];
+      last = p.entry[e + 1].units;
     }
-    const int2 en = p.entry[e];
-    const int32_t tiles = (int32_t)((last - first) / p.Hkv);
-    const int64_t rem = u - first;
-    o.c = (int32_t)(rem / tiles);
-    o.kt0 = (int32_t)(rem % tiles);
+    const int32_t tiles = (int32_t)(last - en.units) / p.Hkv;
+    const int32_t rem = (int32_t)(u - en.units);
+    o.c = rem / tiles;
+    o.kt0 = rem % tiles;
     const int64_t n = min((int64_t)(tiles - o.kt0), uend - u);
     o.kt1 = o.kt0 + (int32_t)n;
     u += n;
-    const SeqRows s = seq_rows(b, en.x);
-    const int32_t packed = s.n * p.g;
-    o.off = en.y * p.tile_rows;
-    o.row0 = s.row0 * p.g + o.off;
-    o.n_rows = min(p.tile_rows, packed - o.off);
-    o.n_keys = s.len;
-    o.see0 = s.len - s.n + 1;
+    o.off = en.rt * p.tile_rows;
+    o.row0 = en.row0 * p.g + o.off;
+    o.n_rows = min(p.tile_rows, en.n * p.g - o.off);
+    o.n_keys = en.len;
+    o.see0 = en.len - en.n + 1;
     o.shared = 0;
-    o.pages = b.page_table + (int64_t)en.x * b.table_stride;
+    o.pages = b.page_table + (int64_t)en.seq * b.table_stride;
     o.partial = p.own_base + (int64_t)p.Hkv * o.row0 + (int64_t)o.c * o.n_rows +
                 (int64_t)p.own_stride * j;
     return true;

@@ -349,6 +349,7 @@ constexpr int kFewRows = 16;
 constexpr int kTcSoftmaxWarps = 4, kTcProducerWarp = 4, kTcQkWarp = 5, kTcPvWarp = 6;
 constexpr int kTcThreads = 224;
 constexpr int kPieceSlots = 4;
+constexpr int kAskAhead = 3;   // tiles
 constexpr int kQBox = 32;   // query rows per TMA box: those of a softmax warp
 constexpr uint64_t kWaitLimitNs = 4000000000ull;   // default: 4 s, far above any legitimate wait
 constexpr uint64_t kDrainLimitNs = 200000000ull;   // 0.2 s for the exit drain
@@ -510,6 +511,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     Piece pc = {};
     walk.u = walk.uend = 0;
     int64_t item = blockIdx.x;
+    int32_t ticket = 0;    // lane 0
+    bool asked = false;
     // The producer alone waits for the kernel before (which rotated the queries
     // and built the plan of the own tokens), and only when it needs them: the
     // first tiles of a prefix piece are loaded before that.  Their pages are
@@ -553,9 +556,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     while (ok) {
       if (!walk.next(p, a.batch, a.prefix_pages, pc)) {
         if (n_pieces > 0 || !PieceWalk::is_shared(p, item)) enter();
-        if (n_pieces > 0) {   // asked for only now, so that slow SMs take fewer
-          int32_t ticket = 0;
-          if (lane == 0) ticket = atomicAdd(&p.head->ticket, 1);
+        if (n_pieces > 0) {
+          if (!asked && lane == 0) ticket = atomicAdd(&p.head->ticket, 1);
+          asked = false;
           item = p.n_ctas + (int64_t)__shfl_sync(kFull, ticket, 0);
         }
         if (!walk.start(p, item) || !walk.next(p, a.batch, a.prefix_pages, pc)) break;
@@ -574,6 +577,12 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       // in the order of their use: K of a tile, then V of the tile before
       int page = -1, next = -1, y = 0, next_y = 0;
       for (int kt = pc.kt0; kt <= pc.kt1; ++kt) {
+        // The next ticket is asked for with the item's last tiles: not earlier, so
+        // that slow SMs take fewer, and not after them, so that it is there in time.
+        if (!asked && entered && walk.u == walk.uend && kt >= pc.kt1 - kAskAhead) {
+          if (lane == 0) ticket = atomicAdd(&p.head->ticket, 1);
+          asked = true;
+        }
         // Q after the first K (whose slot is free before Q's place is), or, in
         // the first piece, once no K slot is left to fill
         if (hold_q && kt == pc.kt0 + (n == 0 ? C::NK : 1)) {
