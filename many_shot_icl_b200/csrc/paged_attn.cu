@@ -17,15 +17,17 @@ namespace dbsa {
 namespace {
 
 // ------------------------------------------------------ fp32 kernel
-// fp32 caches are attended to in fp32 on the CUDA cores: tiles of 32 packed rows
+// fp32 caches are attended to in fp32 on the CUDA cores: tiles of 64 packed rows
 // against 64 keys in shared memory, two CTAs of eight warps per SM.
 //
-// A warp owns four rows and one of KG groups of a tile's keys, and keeps its own
+// A warp owns R rows and one of KG groups of a tile's keys, and keeps its own
 // running maximum, sums and outputs (lanes on columns); the groups are put
-// together once, at the end of the piece.  KG follows the piece's rows (4 rows:
-// 8 groups, .., more than 16: 1), so that a decode step, whose 4 rows would give
-// one warp everything, keeps all eight busy.  For the scores a lane has two keys
-// (KG = 1), one, or the D / 2 or D / 4 dimensions of one.
+// together once, at the end of the piece.  Both follow the piece's rows: more
+// than 32, R = 8, where each K and V read serves eight rows and the FMA units are
+// the limit (with 4 it was the shared memory); 17 to 32, R = 4; below, R = 4 and
+// KG = 2, 4 or 8, so that a decode step, whose 4 rows would give one warp
+// everything, keeps all eight busy.  For the scores a lane has two keys (KG = 1),
+// one, or the D / 2 or D / 4 dimensions of one.
 //
 // K of the next tile is fetched (cp.async) once the scores are done, V once the
 // outputs are, each while the other half of a tile is computed.  The other CTA
@@ -33,17 +35,20 @@ namespace {
 // each K and V read) with many rows, memory with few.  Measured: 1 sequence of 32
 // / 8 heads behind 90k tokens 137 us (0.82 of the copy bandwidth), 8 prompts of
 // ~30 tokens behind 4k 577 us (0.4 of the FMA rate).
-constexpr int kF32Rows = 32, kF32Keys = 64, kF32Warps = 8, kF32Threads = 32 * kF32Warps;
+constexpr int kF32Rows = 64, kF32Keys = 64, kF32Warps = 8, kF32Threads = 32 * kF32Warps;
 
 template <int D>
 struct F32Smem {
   float q[kF32Rows][D];
   float k[kF32Keys][D + 4];   // rows 4 banks apart: float4 reads by 8 lanes do not collide
   float v[kF32Keys][D];
-  float p[kF32Rows][kF32Keys];
-  float ml[kF32Warps][4][2];
-  int32_t ticket;
+  union {
+    float p[kF32Rows][kF32Keys];
+    float ml[kF32Warps][4][2];   // at the end of a piece
+    int32_t ticket;              // between pieces
+  };
 };
+static_assert(sizeof(F32Smem<128>) <= 115712, "two CTAs per SM");
 
 // 16 bytes to shared memory, zeros where there is no source.
 __device__ __forceinline__ void copy16_async(void *dst, const void *src, bool live) {
@@ -85,7 +90,7 @@ __device__ __forceinline__ void fetch_tile(float *dst, int stride, const void *p
   }
 }
 
-template <int D, int KG>
+template <int D, int KG, int R>
 __device__ __forceinline__ void f32_piece(const AttendArgs &a, const Piece &pc, F32Smem<D> &sm) {
   constexpr int V = D / 32, RG = kF32Warps / KG;
   constexpr int KPW = kF32Keys / KG;                // keys of a tile per warp
@@ -93,7 +98,7 @@ __device__ __forceinline__ void f32_piece(const AttendArgs &a, const Piece &pc, 
   constexpr int PARTS = KPW < 32 ? 32 / KPW : 1;    // lanes per key
   const AttendPlan &p = a.plan;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rg = warp % RG, kg = warp / RG, row0 = rg * 4;
+  const int rg = warp % RG, kg = warp / RG, row0 = rg * R;
   const int key_l = kg * KPW + lane % (KPW < 32 ? KPW : 32), part = lane / (KPW < 32 ? KPW : 32);
 
   int page = row_page(pc, a.pool, pc.kt0 * kF32Keys);
@@ -101,10 +106,10 @@ __device__ __forceinline__ void f32_piece(const AttendArgs &a, const Piece &pc, 
   copy_commit();
   fetch_tile<D>(&sm.v[0][0], D, a.pool.v, pc, a.pool, pc.kt0 * kF32Keys, page);
   copy_commit();
-  float m[4], l[4], o[4][V];
-  int seen[4];
+  float m[R], l[R], o[R][V];
+  int seen[R];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < R; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
     seen[i] = row0 + i < pc.n_rows ? keys_seen(pc, p.g, row0 + i) : 0;
@@ -125,7 +130,7 @@ __device__ __forceinline__ void f32_piece(const AttendArgs &a, const Piece &pc, 
     }
     copy_wait_1();
     __syncthreads();   // K is in
-    float s[4][NK] = {};
+    float s[R][NK] = {};
 #pragma unroll 4
     for (int ch = 0; ch < D / 4 / PARTS; ++ch) {
       const int d = (part + PARTS * ch) * 4;
@@ -133,7 +138,7 @@ __device__ __forceinline__ void f32_piece(const AttendArgs &a, const Piece &pc, 
 #pragma unroll
       for (int j = 0; j < NK; ++j) kk[j] = *reinterpret_cast<const float4 *>(&sm.k[key_l + 32 * j][d]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < R; ++i) {
         const float4 x = *reinterpret_cast<const float4 *>(&sm.q[row0 + i][d]);
 #pragma unroll
         for (int j = 0; j < NK; ++j)
@@ -147,7 +152,7 @@ __device__ __forceinline__ void f32_piece(const AttendArgs &a, const Piece &pc, 
     }
     copy_commit();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
       float mt = -INFINITY;
 #pragma unroll
       for (int j = 0; j < NK; ++j) {
@@ -176,11 +181,11 @@ __device__ __forceinline__ void f32_piece(const AttendArgs &a, const Piece &pc, 
     }
     copy_wait_1();
     __syncthreads();   // V is in (and this warp's p)
-#pragma unroll 4
+#pragma unroll 2
     for (int k = 0; k < KPW; k += 4) {
-      float4 pr[4];
+      float4 pr[R];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < R; ++i)
         pr[i] = *reinterpret_cast<const float4 *>(&sm.p[row0 + i][kg * KPW + k]);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
@@ -197,7 +202,7 @@ __device__ __forceinline__ void f32_piece(const AttendArgs &a, const Piece &pc, 
           v[1] = x.y;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < R; ++i) {
           const float w = kk == 0 ? pr[i].x : kk == 1 ? pr[i].y : kk == 2 ? pr[i].z : pr[i].w;
 #pragma unroll
           for (int e = 0; e < V; ++e) o[i][e] += w * v[e];
@@ -209,16 +214,17 @@ __device__ __forceinline__ void f32_piece(const AttendArgs &a, const Piece &pc, 
     copy_commit();
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) l[i] += __shfl_xor_sync(~0u, l[i], d);
   if constexpr (KG > 1) {
+    static_assert(R == 4, "the exchange holds four rows a warp");
     // put the key groups together: group kg's outputs in the idle K tile
     float *part_o = &sm.k[0][0];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) part_o[(warp * 4 + i) * D + lane * V + e] = o[i][e];
+      for (int e = 0; e < V; ++e) part_o[(warp * R + i) * D + lane * V + e] = o[i][e];
       if (lane == 0) {
         sm.ml[warp][i][0] = m[i];
         sm.ml[warp][i][1] = l[i];
@@ -227,7 +233,7 @@ __device__ __forceinline__ void f32_piece(const AttendArgs &a, const Piece &pc, 
     __syncthreads();
     if (kg == 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < R; ++i) {
         float M = m[i];
 #pragma unroll
         for (int g = 1; g < KG; ++g) M = fmaxf(M, sm.ml[rg + g * RG][i][0]);
@@ -242,7 +248,7 @@ __device__ __forceinline__ void f32_piece(const AttendArgs &a, const Piece &pc, 
           f = exp2f(sm.ml[w][i][0] - mu);
           l[i] += f * sm.ml[w][i][1];
 #pragma unroll
-          for (int e = 0; e < V; ++e) o[i][e] += f * part_o[(w * 4 + i) * D + lane * V + e];
+          for (int e = 0; e < V; ++e) o[i][e] += f * part_o[(w * R + i) * D + lane * V + e];
         }
         m[i] = M;
       }
@@ -250,7 +256,7 @@ __device__ __forceinline__ void f32_piece(const AttendArgs &a, const Piece &pc, 
   }
   if (kg == 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
       const int r = row0 + i;
       if (r >= pc.n_rows) break;
       float *dst = p.acc + (pc.partial + r) * D + lane * V;
@@ -283,17 +289,19 @@ __global__ void __launch_bounds__(kF32Threads, 2) attend_f32_kernel(const __grid
     }
     __syncthreads();   // the piece before is done with shared memory
     const float *qs = static_cast<const float *>(p.q_rot) + ((int64_t)pc.c * p.rows + pc.row0) * D;
-    for (int i = tid; i < kF32Rows * CH; i += kF32Threads) {
+    const int rows = pc.n_rows > 32 ? 64 : pc.n_rows > 16 ? 32 : 16;   // that are read
+    for (int i = tid; i < rows * CH; i += kF32Threads) {
       const int r = i / CH, d = (i % CH) * 4;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < pc.n_rows) x = *reinterpret_cast<const float4 *>(qs + (int64_t)r * D + d);
       *reinterpret_cast<float4 *>(&sm.q[r][d]) = x;
     }
     // (the first barrier inside orders these writes before their use)
-    if (pc.n_rows <= 4) f32_piece<D, 8>(a, pc, sm);
-    else if (pc.n_rows <= 8) f32_piece<D, 4>(a, pc, sm);
-    else if (pc.n_rows <= 16) f32_piece<D, 2>(a, pc, sm);
-    else f32_piece<D, 1>(a, pc, sm);
+    if (pc.n_rows <= 4) f32_piece<D, 8, 4>(a, pc, sm);
+    else if (pc.n_rows <= 8) f32_piece<D, 4, 4>(a, pc, sm);
+    else if (pc.n_rows <= 16) f32_piece<D, 2, 4>(a, pc, sm);
+    else if (pc.n_rows <= 32) f32_piece<D, 1, 4>(a, pc, sm);
+    else f32_piece<D, 1, 8>(a, pc, sm);
   }
 }
 
