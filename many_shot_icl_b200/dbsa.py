@@ -411,6 +411,8 @@ def _paged_args(cfg: DbsaConfig, k_pages, v_pages, page_table, row_ptr, seq_lens
     if (not row_ptr.is_contiguous() or not seq_lens.is_contiguous()
             or (width > 1 and pt[1] != 1) or not tables.is_contiguous()):
         _refuse("row_ptr, seq_lens and tables must be contiguous, and the rows of page_table")
+    if max(n_rows, n_seqs, pt[0]) > 0x7FFFFFFF:
+        _refuse("a batch of more than 2^31 - 1 rows, sequences or entries between table rows")
     if index < 0 or not (index == v_pages.get_device() == page_table.get_device()
                          == row_ptr.get_device() == seq_lens.get_device() == tables.get_device()):
         _refuse("pages, page_table, row_ptr, seq_lens and tables must be on one CUDA device")

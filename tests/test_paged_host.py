@@ -162,3 +162,17 @@ def test_binding_refuses_tensors_it_cannot_pass(lib):
     refused("int32", page_table=torch.zeros(2, 1, **i32))
     refused("contiguous", row_ptr=torch.zeros(8, **i32)[::2])
     refused("contiguous", tables=torch.zeros(1 << 16, dtype=torch.uint8)[::2])
+
+
+def test_binding_refuses_counts_beyond_32_bits(lib):
+    """A row that is repeated by a stride of 0 makes such a count without the memory."""
+    i32 = dict(dtype=torch.int32)
+    pages = torch.zeros(4, 2, 64, 128, dtype=torch.bfloat16)
+    row = torch.zeros(1, 2, 128, dtype=torch.bfloat16)
+    for n in (2**31, 2**32 + 1):
+        rows = row.expand(n, 2, 128)
+        with pytest.raises(dbsa.DbsaError) as e:
+            dbsa.paged_append(CFG, rows, rows, pages, pages, torch.zeros(1, 1, **i32),
+                              torch.zeros(2, **i32), torch.zeros(1, **i32),
+                              torch.zeros(1 << 16, dtype=torch.uint8))
+        assert e.value.status == dbsa.ERR_INVALID_ARG and "rows" in str(e.value)
