@@ -361,7 +361,7 @@ dbsa_status dbsa_rope_tables(const dbsa_config *cfg, int64_t n_pos, void *tables
  *          slices of a fused projection and the head-major Stage-1 cache
  *          (row_stride = head_dim, head_stride = cap * head_dim) can both be
  *          the source.  They may not overlap the pages.
- * A slot named by two rows of one call ends up with either one's values.
+ * A slot named by two rows of one call ends up with elements of both.
  * Needs no workspace.
  * Errors: INVALID_ARG (null or misaligned pointer, bad sizes or strides,
  * tables too small for the positions), UNSUPPORTED (cfg, page_size), CUDA. */
@@ -375,8 +375,8 @@ dbsa_status dbsa_paged_append(const dbsa_config *cfg, const void *k, int64_t k_r
  * own sequences: row i (own token t, position prefix_len + t) attends to the
  * prefix tokens 0 .. prefix_len - 1 and to own tokens 0 .. t, whose keys and
  * values are in the cache already (dbsa_paged_append before it, on the same
- * stream).  The prefix is read once per 128 query rows of a KV head (32 with
- * DBSA_F32), whichever sequences they belong to.
+ * stream).  The prefix is read once per 128 query rows of a KV head (64 or
+ * fewer with DBSA_F32), whichever sequences they belong to.
  *   q            device, pre-RoPE: row r, head h at r * q_row_stride + h *
  *                head_dim (q_row_stride a multiple of 8)
  *   prefix_pages device, [ceil(prefix_len / page_size)] page ids (may be NULL
@@ -385,7 +385,8 @@ dbsa_status dbsa_paged_append(const dbsa_config *cfg, const void *k, int64_t k_r
  *                (padding, or every page missing) get 0
  *   workspace    device, 256-byte aligned, ws_bytes >=
  *                dbsa_shared_prefix_workspace_size(); its contents need not be
- *                kept between calls.  Calls that may overlap on the GPU (other
+ *                kept between calls, and one that is large enough for the most
+ *                sequences, rows and prefix serves every smaller call.  Calls that may overlap on the GPU (other
  *                streams, graphs replayed at once) need one each.
  * Slots of a page at or past its sequence's length may hold anything, NaN
  * included.  Keys and values of tokens inside a length must be finite.

@@ -486,6 +486,7 @@ dbsa_status check_paged(const dbsa_config *cfg, const dbsa_paged_cache *cache,
 // ~4 us, writing and merging the partials of a row ~0.17 ns x D / 128 of all CTAs'
 // time.  (More, shorter ranges would also even out the SMs' unequal speeds, but
 // behind 90k tokens one row tile takes 69 us with one wave, 75 with two.)
+constexpr int kMaxWaves = 8;
 int prefix_groups(int rows, int n_row_tiles, int n_ctas, int Hkv, int D, int64_t units) {
   constexpr double kTile = 1.4, kPiece = 4.0, kRow = 0.17e-3;   // us
   int best = 1;
@@ -501,7 +502,8 @@ int prefix_groups(int rows, int n_row_tiles, int n_ctas, int Hkv, int D, int64_t
     }
   };
   for (int cut = 64; cut > 1; cut /= 2) consider(n_ctas / n_row_tiles / cut);   // part of a wave
-  for (int64_t w = 1; w <= 8; ++w) consider(w * n_ctas / n_row_tiles);
+  for (int64_t w = 1; w <= std::min(n_row_tiles, kMaxWaves); ++w)
+    consider(w * n_ctas / n_row_tiles);
   return best;
 }
 
@@ -511,7 +513,8 @@ struct AttendLayout {
 };
 AttendLayout attend_layout(const dbsa_config *cfg, int32_t n_seqs, int32_t n_rows,
                            int64_t prefix_len) {
-  const AttendShape shape = attend_shape(cfg);
+  const int rows = n_rows * (cfg->n_q_heads / cfg->n_kv_heads);
+  const AttendShape shape = attend_shape(cfg, rows, prefix_len);
   AttendLayout l{};
   AttendPlan &p = l.p;
   p.g = cfg->n_q_heads / cfg->n_kv_heads;
@@ -520,7 +523,7 @@ AttendLayout attend_layout(const dbsa_config *cfg, int32_t n_seqs, int32_t n_row
   p.tile_rows = shape.tile_rows;
   p.tile_keys = shape.tile_keys;
   p.n_ctas = shape.n_ctas;
-  p.rows = n_rows * p.g;
+  p.rows = rows;
   p.n_row_tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
   p.prefix_len = (int32_t)prefix_len;
   p.prefix_tiles = (int32_t)((prefix_len + p.tile_keys - 1) / p.tile_keys);
@@ -531,7 +534,18 @@ AttendLayout attend_layout(const dbsa_config *cfg, int32_t n_seqs, int32_t n_row
   p.own_base = prefix_len == 0 ? 0 : (int64_t)(p.Hkv + p.n_groups) * p.rows;
   p.own_ranges = kOwnWaves * p.n_ctas;
   p.own_stride = std::min(p.tile_rows, p.rows);
-  p.partial_rows = p.own_base + (int64_t)p.Hkv * p.rows + (int64_t)p.own_stride * p.own_ranges;
+  // Space is taken for at least what any smaller call needs, so that a workspace
+  // made for the largest batch serves them all: prefix_groups() is not monotone,
+  // nor is the choice of tile_rows.
+  const int64_t units = (int64_t)p.Hkv * p.prefix_tiles, rows64 = rows;
+  const int64_t prefix_rows =   // of n_groups * rows
+      units == 0 ? 0
+                 : std::max(rows64, std::min({units * rows64, p.n_ctas * rows64,
+                                              (int64_t)kMaxWaves * p.n_ctas * shape.max_tile_rows}));
+  const int64_t partial_rows =
+      (int64_t)p.Hkv * rows * (units == 0 ? 1 : 2) + prefix_rows +
+      (int64_t)std::min(shape.max_tile_rows, rows) * p.own_ranges;
+  const size_t max_entries = (size_t)n_seqs + rows / shape.min_tile_rows;
   const size_t elt = cfg->dtype == DBSA_F32 ? 4 : 2;
   size_t off = kStatusBytes;
   auto take = [&](size_t bytes) {
@@ -542,10 +556,10 @@ AttendLayout attend_layout(const dbsa_config *cfg, int32_t n_seqs, int32_t n_row
   l.head = take(sizeof(PlanHead));
   l.row_info = take((size_t)n_rows * sizeof(int4));
   l.first_entry = take(((size_t)n_seqs + 1) * sizeof(int32_t));
-  l.entry = take(((size_t)p.max_entries + 1) * sizeof(Entry));
+  l.entry = take((max_entries + 1) * sizeof(Entry));
   l.q_rot = take((size_t)p.Hkv * p.rows * p.D * elt);
-  l.acc = take((size_t)p.partial_rows * p.D * sizeof(float));
-  l.ml = take((size_t)p.partial_rows * sizeof(float2));
+  l.acc = take((size_t)partial_rows * p.D * sizeof(float));
+  l.ml = take((size_t)partial_rows * sizeof(float2));
   l.total = align_up(off);
   return l;
 }

@@ -116,15 +116,14 @@ struct AttendPlan {
   int32_t own_stride;      // rows an own-token entry has at most
   int32_t max_entries;     // own-token (sequence, row tile) entries, at most
   int64_t own_base;        // first own-token partial row
-  int64_t partial_rows;
   // device
   PlanHead *head;
   int4 *row_info;          // [n_rows]: row_token(): sequence, token, its first row, its rows
   int32_t *first_entry;    // [n_seqs + 1]
   Entry *entry;            // [max_entries + 1]
   void *q_rot;             // [Hkv][rows][D], cfg->dtype, rotated
-  float *acc;              // [partial_rows][D], not normalised
-  float2 *ml;              // [partial_rows]: (maximum in log2 units, sum)
+  float *acc;              // [partial rows][D], not normalised
+  float2 *ml;              // [partial rows]: (maximum in log2 units, sum)
 };
 
 // One piece: rows of a tile against key tiles [kt0, kt1) of one list of pages.

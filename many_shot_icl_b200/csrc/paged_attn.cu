@@ -931,9 +931,20 @@ cudaError_t launch_tc(const AttendArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-AttendShape attend_shape(const dbsa_config *cfg) {
-  if (cfg->dtype == DBSA_F32) return {kF32Rows, kF32Keys, 2 * 148};
-  return {kTcRows, kTcKeys, 2 * 148};
+AttendShape attend_shape(const dbsa_config *cfg, int rows, int64_t prefix_len) {
+  constexpr int n_ctas = 2 * 148;
+  if (cfg->dtype != DBSA_F32) return {kTcRows, kTcKeys, n_ctas, kTcRows, kTcRows};
+  // fp32: a tile costs what its rows cost, so work that fits one wave of smaller
+  // tiles takes those (25 rows x 32 heads behind 71 tokens: 29 us with 64-row
+  // tiles).  One more key tile stands for the own tokens, whose lengths the host
+  // does not know; tiles of less than 16 rows would read long ones too often.
+  constexpr int least = 16;
+  int tile_rows = least;
+  const int64_t keys = (prefix_len + kF32Keys - 1) / kF32Keys + 1;
+  while (tile_rows < kF32Rows &&
+         (rows + tile_rows - 1) / tile_rows * keys * cfg->n_kv_heads > n_ctas)
+    tile_rows *= 2;
+  return {tile_rows, kF32Keys, n_ctas, least, kF32Rows};
 }
 
 cudaError_t launch_attend_pieces(const AttendArgs &a, int head_dim, bool f32, cudaStream_t st) {

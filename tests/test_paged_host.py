@@ -137,6 +137,20 @@ def test_sizes(lib):
     assert call(ctypes.byref(c), 16, FAKE, 100, None) == dbsa.ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("heads", [(32, 8, 128), (32, 32, 128), (5, 1, 64)])
+def test_a_workspace_for_the_largest_call_serves_the_smaller_ones(lib, dtype, heads):
+    cfg = dbsa.DbsaConfig(*heads, dtype)
+    for prefix in (0, 1, 100, 4001, 90223):
+        sizes = [dbsa.shared_prefix_workspace_size(cfg, 64, n, prefix) for n in range(1, 700)]
+        assert sizes == sorted(sizes)
+    for rows in (1, 3, 64, 641):
+        sizes = [dbsa.shared_prefix_workspace_size(cfg, n, rows, 1000) for n in range(1, 300)]
+        assert sizes == sorted(sizes)
+        sizes = [dbsa.shared_prefix_workspace_size(cfg, 8, rows, n) for n in range(0, 9000, 17)]
+        assert sizes == sorted(sizes)
+
+
 def test_binding_refuses_tensors_it_cannot_pass(lib):
     """Types, shapes and strides are checked before the device is asked for."""
     i32 = dict(dtype=torch.int32)
