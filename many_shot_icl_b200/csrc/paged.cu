@@ -249,8 +249,11 @@ __global__ void __launch_bounds__(256) attend_prep_kernel(const AttendArgs a) {
 // -> the own partials; the prefix's partials are known from the arguments and are
 // read meanwhile.  W is the number of pieces over four: with W = 4 throughout, 256
 // rows of 32 heads with 7 pieces each took 34 us; a warp per (row, head) took 50 us
-// for 2 000 rows of 32 heads with 2 or 3.
+// for 2 000 rows of 32 heads with 2 or 3.  But few rows (one warp per scheduler or
+// less) leave the SMs idle while a warp does its heads in turn: 42 rows of 32 heads
+// took 10.8 us with W = 1, 6.0 with 2.
 constexpr int kMergeWarps = 4;
+constexpr int kFewMergeRows = 4 * 148;
 
 template <int D, typename T, int W>
 __global__ void __launch_bounds__(32 * kMergeWarps) attend_merge_kernel(const AttendArgs a) {
@@ -597,7 +600,8 @@ cudaError_t launch_attend_t(const AttendArgs &a, cudaStream_t st) {
                       st, a);
   };
   if (pieces > 12) return merge(attend_merge_kernel<D, T, 4>, 4);
-  if (pieces > 8) return merge(attend_merge_kernel<D, T, 2>, 2);
+  if (pieces > 8 || (int64_t)a.batch.n_rows * a.plan.Hkv <= kFewMergeRows)
+    return merge(attend_merge_kernel<D, T, 2>, 2);
   return merge(attend_merge_kernel<D, T, 1>, 1);
 }
 
