@@ -23,18 +23,18 @@ namespace {
 // A warp owns R rows and one of KG groups of a tile's keys, and keeps its own
 // running maximum, sums and outputs (lanes on columns); the groups are put
 // together once, at the end of the piece.  Both follow the piece's rows: more
-// than 32, R = 8, where each K and V read serves eight rows and the FMA units are
-// the limit (with 4 it was the shared memory); 17 to 32, R = 4; below, R = 4 and
+// than 32, R = 8, where each K and V read serves eight rows (with 4 the shared
+// memory was the limit: prompts 589 us for 541); 17 to 32, R = 4; below, R = 4 and
 // KG = 2, 4 or 8, so that a decode step, whose 4 rows would give one warp
 // everything, keeps all eight busy.  For the scores a lane has two keys (KG = 1),
 // one, or the D / 2 or D / 4 dimensions of one.
 //
 // K of the next tile is fetched (cp.async) once the scores are done, V once the
 // outputs are, each while the other half of a tile is computed.  The other CTA
-// of the SM fills the waits.  Bound: FMA and shared-memory reads (four rows share
-// each K and V read) with many rows, memory with few.  Measured: 1 sequence of 32
-// / 8 heads behind 90k tokens 137 us (0.82 of the copy bandwidth), 8 prompts of
-// ~30 tokens behind 4k 577 us (0.4 of the FMA rate).
+// of the SM fills the waits.  Bound: FMA and shared-memory reads (about even at
+// R = 8) with many rows, memory with few.  Measured: 1 sequence of 32
+// / 8 heads behind 90k tokens 140 us (0.81 of the copy bandwidth), 8 prompts of
+// ~30 tokens behind 4k 541 us (0.4 of the FMA rate).
 constexpr int kF32Rows = 64, kF32Keys = 64, kF32Warps = 8, kF32Threads = 32 * kF32Warps;
 
 template <int D>
