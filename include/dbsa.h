@@ -327,7 +327,9 @@ dbsa_status dbsa_gather_rope_attend_noalloc(
  *
  * Both calls read RoPE angle tables that dbsa_rope_tables() has written once
  * for cfg (its head_dim and rope_theta); they must cover every position a call
- * can reach, pos0 (prefix_len) + table_width * page_size.
+ * can reach, pos0 (prefix_len) + table_width * page_size.  A call takes
+ * tables_bytes for what has been written: fewer bytes than that are fine (the
+ * angles of a position do not move), more claim positions that were not.
  * ------------------------------------------------------------------------ */
 typedef struct dbsa_paged_cache {
     void *k_pages, *v_pages; /* device, 16-byte aligned, cfg->dtype */
@@ -348,7 +350,8 @@ typedef struct dbsa_paged_batch {
 } dbsa_paged_batch;
 
 /* Bytes of the angle tables for positions [0, n_pos), 0 on bad arguments; and
- * the kernel that fills them (`tables`: device, 16-byte aligned). */
+ * the kernel that fills them (`tables`: device, 16-byte aligned), all
+ * tables_bytes, which may be more. */
 size_t dbsa_rope_tables_size(const dbsa_config *cfg, int64_t n_pos);
 dbsa_status dbsa_rope_tables(const dbsa_config *cfg, int64_t n_pos, void *tables,
                              size_t tables_bytes, void *stream);

@@ -86,6 +86,13 @@ cudaError_t launch_rope_tables(float *base, int32_t n_hi, int32_t head_dim, doub
 // Table pointers inside a block of rope_table_bytes() starting at `base`.
 RopeTables rope_tables_at(const float *base, int32_t n_hi, int32_t head_dim);
 size_t rope_table_bytes(int32_t n_hi, int32_t head_dim);
+// The same angles in as many bytes, for tables that outlive a call: lc, ls, then
+// one row of cosines and sines per 16 positions, so that no place depends on n_hi
+// and a buffer reads the same whatever part of it a call is given.  hc and hs have
+// rows D apart: read them at position rope_row_pos(p).
+cudaError_t launch_rope_rows(float *base, int32_t n_hi, int32_t head_dim, double theta,
+                             cudaStream_t st);
+RopeTables rope_rows_at(const float *base, int32_t head_dim);
 
 // Rotate K of n_tok token-major input rows (positions pos0..), copy the raw
 // K/V into the cache rows pos0.., and (f32 inputs) write bf16 V.  (The

@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs<T> a) {
                          (t.token >> a.pool.page_shift));
   if (page < 0 || page >= a.pool.n_pages) return;
   float cs[8], sn[8];
-  rope_cs8(a.rope, a.pos0 + t.token, i0, H, cs, sn);
+  rope_cs8(a.rope, rope_row_pos(a.pos0 + t.token), i0, H, cs, sn);
   rotate8(lo, hi, cs, sn);
   const int64_t dst =
       page * a.pool.page_stride +
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(256) attend_prep_kernel(const AttendArgs a) {
   const RowToken t = row_token(a.batch, row);
   if (c == 0 && cp == 0) p.row_info[row] = make_int4(t.seq, t.token, t.rows.row0, t.rows.n);
   const bool live = t.seq >= 0 && t.token >= 0;   // other rows: finite, never used
-  rope_cs8(a.rope, live ? (int64_t)p.prefix_len + t.token : 0, i0, H, cs, sn);
+  rope_cs8(a.rope, rope_row_pos(live ? (int64_t)p.prefix_len + t.token : 0), i0, H, cs, sn);
   for (int hl = 0; hl < p.g; hl += 2) {
     if (hl > 0) load(hl);
 #pragma unroll
@@ -477,8 +477,7 @@ dbsa_status check_paged(const dbsa_config *cfg, const dbsa_paged_cache *cache,
   batch->table_width = b->table_width;
   batch->table_stride = b->table_stride;
   batch->cap = (int32_t)own_cap;
-  const int64_t n_hi = table_positions(cfg, tables_bytes) / kRopeLo;
-  *rope = rope_tables_at(static_cast<const float *>(tables), (int32_t)n_hi, cfg->head_dim);
+  *rope = rope_rows_at(static_cast<const float *>(tables), cfg->head_dim);
   return DBSA_OK;
 }
 
@@ -650,11 +649,11 @@ dbsa_status dbsa_rope_tables(const dbsa_config *cfg, int64_t n_pos, void *tables
     return fail(DBSA_ERR_INVALID_ARG, "tables is NULL or not 16-byte aligned");
   if (tables_bytes < need)
     return fail(DBSA_ERR_INVALID_ARG, "tables too small: %zu < %zu bytes", tables_bytes, need);
-  // every position the buffer has room for, so that its size alone says which
-  // positions it covers
+  // every position the bytes have room for: the calls take their size for the
+  // positions that are covered
   const int32_t n_hi = (int32_t)(table_positions(cfg, tables_bytes) / kRopeLo);
-  const cudaError_t e = launch_rope_tables(static_cast<float *>(tables), n_hi, cfg->head_dim,
-                                           cfg->rope_theta, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_rope_rows(static_cast<float *>(tables), n_hi, cfg->head_dim,
+                                         cfg->rope_theta, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rope tables");
   count_launches(1);
   return DBSA_OK;

@@ -281,6 +281,12 @@ __device__ __forceinline__ int32_t keys_seen(const Piece &p, int g, int i) {
   return p.shared ? p.n_keys : min(p.n_keys, p.see0 + (p.off + i) / g);
 }
 
+// Where rope_cs8() finds position p in tables laid out by rope_rows_at(): its rows
+// of cosines are every second row of D / 2.
+__device__ __forceinline__ int64_t rope_row_pos(int64_t p) {
+  return (p >> kRopeShift << (kRopeShift + 1)) | (p & (kRopeLo - 1));
+}
+
 struct AttendArgs {
   PagedPool pool;
   PagedBatch batch;

@@ -15,11 +15,11 @@
 namespace dbsa {
 namespace {
 
-__global__ void rope_tables_kernel(float *base, int32_t n_hi, int32_t half, double theta) {
+// `hi_stride`: elements from one row of hc (hs) to the next.
+__global__ void rope_tables_kernel(float *hc, float *hs, float *lc, float *ls, int32_t n_hi,
+                                   int32_t half, int32_t hi_stride, double theta) {
   pdl_enter();
   const int64_t n = (int64_t)(n_hi + kRopeLo) * half;
-  float *hc = base, *hs = hc + (int64_t)n_hi * half;
-  float *lc = hs + (int64_t)n_hi * half, *ls = lc + (int64_t)kRopeLo * half;
   for (int64_t u = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; u < n;
        u += (int64_t)gridDim.x * blockDim.x) {
     const int32_t i = (int32_t)(u % half);
@@ -28,8 +28,8 @@ __global__ void rope_tables_kernel(float *base, int32_t n_hi, int32_t half, doub
     double sn, cs;
     if (row < n_hi) {
       sincos((double)(row * kRopeLo) * w, &sn, &cs);
-      hc[row * half + i] = (float)cs;
-      hs[row * half + i] = (float)sn;
+      hc[row * hi_stride + i] = (float)cs;
+      hs[row * hi_stride + i] = (float)sn;
     } else {
       const int64_t r = row - n_hi;
       sincos((double)r * w, &sn, &cs);
@@ -279,6 +279,16 @@ int grid_for(int64_t n_units, int block) {
   return (int)g;
 }
 
+cudaError_t fill_tables(const RopeTables &t, int32_t n_hi, int32_t head_dim, int32_t hi_stride,
+                        double theta, cudaStream_t st) {
+  const int half = head_dim / 2;
+  const int64_t n = (int64_t)(n_hi + kRopeLo) * half;
+  pdl_launch(rope_tables_kernel, dim3(grid_for(n, 256)), dim3(256), 0, st,
+             const_cast<float *>(t.hc), const_cast<float *>(t.hs), const_cast<float *>(t.lc),
+             const_cast<float *>(t.ls), n_hi, half, hi_stride, theta);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_rel_rope(const RelRopeArgs &a, int head_dim, bool f32, cudaStream_t st) {
@@ -335,12 +345,25 @@ RopeTables rope_tables_at(const float *base, int32_t n_hi, int32_t head_dim) {
   return t;
 }
 
+RopeTables rope_rows_at(const float *base, int32_t head_dim) {
+  const int64_t half = head_dim / 2;
+  RopeTables t;
+  t.lc = base;
+  t.ls = t.lc + kRopeLo * half;
+  t.hc = t.ls + kRopeLo * half;
+  t.hs = t.hc + half;
+  t.n_hi = 0;   // whatever the buffer holds
+  return t;
+}
+
 cudaError_t launch_rope_tables(float *base, int32_t n_hi, int32_t head_dim, double theta,
                                cudaStream_t st) {
-  const int half = head_dim / 2;
-  const int64_t n = (int64_t)(n_hi + kRopeLo) * half;
-  pdl_launch(rope_tables_kernel, dim3(grid_for(n, 256)), dim3(256), 0, st, base, n_hi, half, theta);
-  return cudaGetLastError();
+  return fill_tables(rope_tables_at(base, n_hi, head_dim), n_hi, head_dim, head_dim / 2, theta, st);
+}
+
+cudaError_t launch_rope_rows(float *base, int32_t n_hi, int32_t head_dim, double theta,
+                             cudaStream_t st) {
+  return fill_tables(rope_rows_at(base, head_dim), n_hi, head_dim, head_dim, theta, st);
 }
 
 cudaError_t launch_ingest(const IngestArgs &a, int head_dim, bool f32, cudaStream_t st) {

@@ -428,7 +428,9 @@ def rope_tables_size(cfg: DbsaConfig, n_pos: int) -> int:
 
 def rope_tables(cfg: DbsaConfig, n_pos: int, buf, stream=None):
     """Angle tables for positions [0, n_pos) into buf (uint8 device tensor of
-    rope_tables_size() bytes), for paged_append and shared_prefix_attend."""
+    rope_tables_size() bytes, or more: all of it is filled), for paged_append and
+    shared_prefix_attend, which may be given any part from its start that covers
+    their positions."""
     if buf.get_device() < 0 or not buf.is_contiguous():
         _refuse("buf must be a contiguous CUDA tensor")
     c = cfg.c()
