@@ -393,10 +393,12 @@ dbsa_status dbsa_paged_append(const dbsa_config *cfg, const void *k, int64_t k_r
  *                streams, graphs replayed at once) need one each.
  * Slots of a page at or past its sequence's length may hold anything, NaN
  * included.  Keys and values of tokens inside a length must be finite.
- * Results do not depend on what else is in the workspace, and repeat bit for
- * bit.  DBSA_F32 caches are attended to in fp32; with DBSA_BF16 the rotated
- * queries and the probabilities are rounded to bf16 for the tensor cores, and
- * sums and softmax statistics are fp32.
+ * Results do not depend on what else is in the workspace nor on the values of
+ * other sequences' queries, and repeat bit for bit (how many rows and tokens
+ * there are decides how the work is cut, and so the last bits).  DBSA_F32
+ * caches are attended to in fp32; with DBSA_BF16 the rotated queries and the
+ * probabilities are rounded to bf16 for the tensor cores, and sums and softmax
+ * statistics are fp32.
  * Errors: as dbsa_paged_append, and WORKSPACE. */
 size_t dbsa_shared_prefix_workspace_size(const dbsa_config *cfg, int32_t n_seqs, int32_t n_rows,
                                          int64_t prefix_len);

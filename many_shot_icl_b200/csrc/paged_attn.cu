@@ -805,7 +805,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             // O must hold the tiles before this one
             if (!(ok = wait_warp(C::PV_DONE + (tn - 1) % C::NV, ((tn - 1) / C::NV) & 1))) break;
             tc_fence_after();
-            const float m_new = fmaxf(m_ref, mx);
+            // (rows that need no new reference keep theirs: with another one their
+            // probabilities would round differently, because of a neighbour)
+            const float m_new = mx > m_ref + 8.f ? mx : m_ref;
             const float f = m_new == -INFINITY ? 1.f : ex2(m_ref - m_new);
             l *= f;
             m_ref = m_new;
