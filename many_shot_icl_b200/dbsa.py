@@ -13,7 +13,6 @@ import os
 from dataclasses import dataclass
 
 import numpy as np
-import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdbsa.so")
@@ -175,6 +174,7 @@ def _dp(t) -> int | None:
 
 
 def _stream(stream) -> int:
+    import torch
     s = torch.cuda.current_stream() if stream is None else stream
     return s.cuda_stream
 
@@ -353,10 +353,24 @@ def _refuse(msg: str):
     raise DbsaError(ERR_INVALID_ARG, msg)
 
 
-_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
-_current_device = torch.cuda.current_device
-# (the public stream object costs 2 us, a quarter of a short call)
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# torch and what the paged calls use of it, taken by the first of them: the
+# host-only functions above and the size queries do without.
+torch = _DTYPES = _current_device = _raw_stream = None
+
+
+def _with_torch():
+    """The library, with torch imported."""
+    global torch, _DTYPES, _current_device, _raw_stream
+    lib = load()
+    if torch is None:
+        import torch as t
+        _DTYPES = {"f32": t.float32, "bf16": t.bfloat16}
+        _current_device = t.cuda.current_device
+        # (the public stream object costs 2 us, a quarter of a short call)
+        _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: t.cuda.current_stream(index).cuda_stream)
+        torch = t
+    return lib
 
 
 def _run(fn, index: int, stream, *args):
@@ -434,8 +448,8 @@ def rope_tables(cfg: DbsaConfig, n_pos: int, buf, stream=None):
     if buf.get_device() < 0 or not buf.is_contiguous():
         _refuse("buf must be a contiguous CUDA tensor")
     c = cfg.c()
-    _run(load().dbsa_rope_tables, buf.get_device(), stream, ctypes.byref(c), n_pos, _dp(buf),
-         buf.numel() * buf.element_size())
+    _run(_with_torch().dbsa_rope_tables, buf.get_device(), stream, ctypes.byref(c), n_pos,
+         _dp(buf), buf.numel() * buf.element_size())
 
 
 def paged_append(cfg: DbsaConfig, k, v, k_pages, v_pages, page_table, row_ptr, seq_lens, tables,
@@ -443,8 +457,8 @@ def paged_append(cfg: DbsaConfig, k, v, k_pages, v_pages, page_table, row_ptr, s
     """Append the rows k, v [n_rows][n_kv_heads][head_dim] (any row and head
     stride) of a batch to their sequences' pages, keys rotated at pos0 + their
     index in the sequence (see dbsa_paged_append)."""
-    if _lib is None:
-        load()
+    if torch is None:
+        _with_torch()
     shape, ks, vs, index = k.shape, k.stride(), v.stride(), k_pages.get_device()
     cache, batch = _paged_args(cfg, k_pages, v_pages, page_table, row_ptr, seq_lens, tables,
                                shape[0], index)
@@ -475,8 +489,8 @@ def shared_prefix_attend(cfg: DbsaConfig, q, k_pages, v_pages, prefix_pages, pre
     over a shared prefix and, causally, each row's own sequence, into out of
     the same shape, contiguous (see dbsa_shared_prefix_attend).  prefix_pages
     may be None when prefix_len is 0."""
-    if _lib is None:
-        load()
+    if torch is None:
+        _with_torch()
     shape, st, index, d = q.shape, q.stride(), k_pages.get_device(), cfg.head_dim
     cache, batch = _paged_args(cfg, k_pages, v_pages, page_table, row_ptr, seq_lens, tables,
                                shape[0], index)
