@@ -397,9 +397,9 @@ def _config_ref(cfg: DbsaConfig):
 
 
 def _paged_args(cfg: DbsaConfig, k_pages, v_pages, page_table, row_ptr, seq_lens, tables, n_rows,
-                index):
+                pos0, index):
     """The cache and batch structs of a call on device `index`, after checking
-    the tensors."""
+    the tensors (and the position of the sequences' first tokens)."""
     shape, st, dtype = k_pages.shape, k_pages.stride(), _DTYPES[cfg.dtype]
     if len(shape) != 4 or v_pages.shape != shape:
         _refuse("pages must be [n_pages][n_kv_heads][page_size][head_dim], keys and values alike")
@@ -425,8 +425,12 @@ def _paged_args(cfg: DbsaConfig, k_pages, v_pages, page_table, row_ptr, seq_lens
     if (not row_ptr.is_contiguous() or not seq_lens.is_contiguous()
             or (width > 1 and pt[1] != 1) or not tables.is_contiguous()):
         _refuse("row_ptr, seq_lens and tables must be contiguous, and the rows of page_table")
-    if max(n_rows, n_seqs, pt[0]) > 0x7FFFFFFF:
-        _refuse("a batch of more than 2^31 - 1 rows, sequences or entries between table rows")
+    # (ctypes cuts a number that its C type cannot hold)
+    if max(n_rows, n_seqs, width, pt[0], n_pages) > 0x7FFFFFFF:
+        _refuse("more than 2^31 - 1 pages, rows, sequences, table entries or entries between "
+                "table rows")
+    if not 0 <= pos0 <= 1 << 30:
+        _refuse("positions must start at 0..2^30")
     if index < 0 or not (index == v_pages.get_device() == page_table.get_device()
                          == row_ptr.get_device() == seq_lens.get_device() == tables.get_device()):
         _refuse("pages, page_table, row_ptr, seq_lens and tables must be on one CUDA device")
@@ -435,9 +439,15 @@ def _paged_args(cfg: DbsaConfig, k_pages, v_pages, page_table, row_ptr, seq_lens
                        page_table.data_ptr(), width, pt[0] if n_seqs > 1 else width))
 
 
+def _count(n: int) -> int:
+    """n, or -1, which the library refuses, where its C type might not hold it (no
+    count may be larger)."""
+    return n if 0 <= n <= 1 << 31 else -1
+
+
 def rope_tables_size(cfg: DbsaConfig, n_pos: int) -> int:
     c = cfg.c()
-    return int(load().dbsa_rope_tables_size(ctypes.byref(c), n_pos))
+    return int(load().dbsa_rope_tables_size(ctypes.byref(c), _count(n_pos)))
 
 
 def rope_tables(cfg: DbsaConfig, n_pos: int, buf, stream=None):
@@ -448,7 +458,7 @@ def rope_tables(cfg: DbsaConfig, n_pos: int, buf, stream=None):
     if buf.get_device() < 0 or not buf.is_contiguous():
         _refuse("buf must be a contiguous CUDA tensor")
     c = cfg.c()
-    _run(_with_torch().dbsa_rope_tables, buf.get_device(), stream, ctypes.byref(c), n_pos,
+    _run(_with_torch().dbsa_rope_tables, buf.get_device(), stream, ctypes.byref(c), _count(n_pos),
          _dp(buf), buf.numel() * buf.element_size())
 
 
@@ -461,7 +471,7 @@ def paged_append(cfg: DbsaConfig, k, v, k_pages, v_pages, page_table, row_ptr, s
         _with_torch()
     shape, ks, vs, index = k.shape, k.stride(), v.stride(), k_pages.get_device()
     cache, batch = _paged_args(cfg, k_pages, v_pages, page_table, row_ptr, seq_lens, tables,
-                               shape[0], index)
+                               shape[0], pos0, index)
     dtype = _DTYPES[cfg.dtype]
     if (k.dtype != dtype or v.dtype != dtype or len(shape) != 3 or v.shape != shape
             or shape[1] != cfg.n_kv_heads or shape[2] != cfg.head_dim or ks[2] != 1 or vs[2] != 1):
@@ -479,8 +489,8 @@ def paged_append(cfg: DbsaConfig, k, v, k_pages, v_pages, page_table, row_ptr, s
 def shared_prefix_workspace_size(cfg: DbsaConfig, n_seqs: int, n_rows: int,
                                  prefix_len: int) -> int:
     c = cfg.c()
-    return int(load().dbsa_shared_prefix_workspace_size(ctypes.byref(c), n_seqs, n_rows,
-                                                        prefix_len))
+    return int(load().dbsa_shared_prefix_workspace_size(ctypes.byref(c), _count(n_seqs),
+                                                        _count(n_rows), _count(prefix_len)))
 
 
 def shared_prefix_attend(cfg: DbsaConfig, q, k_pages, v_pages, prefix_pages, prefix_len: int,
@@ -493,7 +503,7 @@ def shared_prefix_attend(cfg: DbsaConfig, q, k_pages, v_pages, prefix_pages, pre
         _with_torch()
     shape, st, index, d = q.shape, q.stride(), k_pages.get_device(), cfg.head_dim
     cache, batch = _paged_args(cfg, k_pages, v_pages, page_table, row_ptr, seq_lens, tables,
-                               shape[0], index)
+                               shape[0], prefix_len, index)
     dtype = _DTYPES[cfg.dtype]
     if (q.dtype != dtype or len(shape) != 3 or shape[1] != cfg.n_q_heads or shape[2] != d
             or st[2] != 1 or (st[1] != d and shape[1] > 1)):
