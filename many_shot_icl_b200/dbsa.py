@@ -413,8 +413,10 @@ def _paged_args(cfg: DbsaConfig, k_pages, v_pages, page_table, row_ptr, seq_lens
     if n_pages == 1:
         stride = hkv * page
         st, vst = (stride, *st[1:]), (stride, *vst[1:])
+    if hkv == 1:
+        st, vst = (st[0], page, *st[2:]), (vst[0], page, *vst[2:])
     if (k_pages.dtype != dtype or v_pages.dtype != dtype or st != vst or st[3] != 1 or st[2] != d
-            or (st[1] != page and hkv > 1)):
+            or st[1] != page):
         _refuse("pages must be %s, contiguous inside a page, with one page stride" % dtype)
     n_seqs, table, pt, i32 = seq_lens.numel(), page_table.shape, page_table.stride(), torch.int32
     if (row_ptr.dtype != i32 or seq_lens.dtype != i32 or page_table.dtype != i32

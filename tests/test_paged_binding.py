@@ -64,3 +64,21 @@ def test_sizes_beyond_their_c_types():
     assert size(CFG, 3, 5, 2 ** 64 + 100) == 0
     assert size(CFG, 3, 5, -2 ** 64) == 0
     assert size(CFG, 3, 5, 100) > 0
+
+
+@pytest.mark.parametrize("name", ["append", "attend"])
+def test_the_stride_of_a_dimension_of_one_means_nothing(name):
+    """One KV head, its pages taken from [page][token][head][d] pools: the strides
+    of keys and values differ only where there is nothing to step over."""
+    cfg = dbsa.DbsaConfig(8, 1, 128)
+    k = torch.zeros(4, 64, 1, 128, dtype=torch.bfloat16).transpose(1, 2)
+    v = torch.zeros(4, 1, 64, 128, dtype=torch.bfloat16)
+    assert k.stride() != v.stride()
+    assert "CUDA device" in call(name, cfg, k_pages=k, v_pages=v)
+    assert "CUDA device" in call(name, cfg, k_pages=v, v_pages=k)
+    assert "CUDA device" in call(name, cfg, k_pages=k[:1], v_pages=v[:1])
+    # what does mean something still has to be alike
+    assert "page stride" in call(name, cfg, k_pages=k,
+                                 v_pages=torch.zeros(8, 1, 64, 128, dtype=torch.bfloat16)[::2])
+    two = torch.zeros(4, 64, 2, 128, dtype=torch.bfloat16).transpose(1, 2)
+    assert "contiguous inside" in call(name, CFG, k_pages=two, v_pages=two)
