@@ -91,14 +91,6 @@ float scale_log2(const dbsa_config *cfg) {
   return (float)(s * 1.4426950408889634);  // * log2(e)
 }
 
-int num_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    return 148;
-  return n;
-}
-
 dbsa_status check_ws(void *ws, size_t ws_bytes, size_t need) {
   if (ws == nullptr) return fail(DBSA_ERR_WORKSPACE, "workspace is NULL");
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
@@ -111,6 +103,14 @@ dbsa_status check_ws(void *ws, size_t ws_bytes, size_t need) {
 }  // namespace dbsa
 
 namespace {
+
+int num_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return 148;
+  return n;
+}
 
 constexpr size_t kAlign = 1024;
 // Block-major passes with at most this many query rows per (query, KV head)

@@ -276,7 +276,6 @@ dbsa_status cuda_fail(cudaError_t e, const char *where);
 dbsa_status check_cfg(const dbsa_config *cfg);
 dbsa_status check_ws(void *ws, size_t ws_bytes, size_t need);
 float scale_log2(const dbsa_config *cfg);
-int num_sms();
 void count_launches(int n);
 uint64_t take_wait_expiry();   // the limit dbsa_test_wait_expiry() set, cleared
 // Records the profiling events (if any) around the main kernel of a call.
