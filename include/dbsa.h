@@ -313,7 +313,8 @@ dbsa_status dbsa_gather_rope_attend_noalloc(
  *
  * The arrays of a batch are DEVICE arrays, read by the kernels: a call can be
  * captured into a CUDA graph (after one like it outside of capture, which loads
- * the kernels) and replayed after they have changed.  Their contents are not checked on the host; the kernels check every index:
+ * the kernels) and replayed after they have changed.  Their contents are not
+ * checked on the host; the kernels check every index:
  *  - rows [row_ptr[s], row_ptr[s+1]) of the batch belong to sequence s; row_ptr
  *    must not decrease.  A sequence whose rows are not inside [0, n_rows] has
  *    no rows.  Rows of no sequence are ignored, and their outputs left as
@@ -384,13 +385,14 @@ dbsa_status dbsa_paged_append(const dbsa_config *cfg, const void *k, int64_t k_r
  *                head_dim (q_row_stride a multiple of 8)
  *   prefix_pages device, [ceil(prefix_len / page_size)] page ids (may be NULL
  *                when prefix_len is 0)
- *   out          device, [n_rows][Hq][D], apart from the inputs; rows that may attend to nothing
- *                (padding, or every page missing) get 0
+ *   out          device, [n_rows][Hq][D], apart from the inputs; rows that may
+ *                attend to nothing (padding, or every page missing) get 0
  *   workspace    device, 256-byte aligned, ws_bytes >=
  *                dbsa_shared_prefix_workspace_size(); its contents need not be
  *                kept between calls, and one that is large enough for the most
- *                sequences, rows and prefix serves every smaller call.  Calls that may overlap on the GPU (other
- *                streams, graphs replayed at once) need one each.
+ *                sequences, rows and prefix serves every smaller call.  Calls
+ *                that may overlap on the GPU (other streams, graphs replayed at
+ *                once) need one each.
  * Slots of a page at or past its sequence's length may hold anything, NaN
  * included.  Keys and values of tokens inside a length must be finite.
  * Results do not depend on what else is in the workspace nor on the values of

@@ -43,8 +43,9 @@ struct Raw8 {
 // D/2] cos + k[i] sin; v is copied.  Every element is read and written once:
 // the kernel is bound by memory (long appends) or by the latency of its chain
 // row -> sequence -> page -> store (decode steps).  Measured, 8 heads of 128,
-// bf16: 90 223 tokens from the head-major cache 118 us (6.3 TB/s read and written,
-// 0.96 of the copy bandwidth), 64 single tokens 2.5 us.  A block takes 256 / (D/16)
+// bf16, in short runs: 90 223 tokens from the head-major cache 118 us (6.3 TB/s
+// read and written, 0.96 of the copy bandwidth; 123 us, 0.92, back to back at the
+// power limit), 64 single tokens 2.6 us.  A block takes 256 / (D/16)
 // rows of one KV head; a thread 8 rotation pairs of the row's key and the
 // matching 16 elements of its value.
 template <typename T>
@@ -247,11 +248,13 @@ __global__ void __launch_bounds__(256) attend_prep_kernel(const AttendArgs a) {
 // Four warps a block, four pieces in flight per warp, lanes hold the columns.
 // Bound by the latency of its chain of reads (L2): the row's record -> its entry
 // -> the own partials; the prefix's partials are known from the arguments and are
-// read meanwhile.  W is the number of pieces over four: with W = 4 throughout, 256
-// rows of 32 heads with 7 pieces each took 34 us; a warp per (row, head) took 50 us
-// for 2 000 rows of 32 heads with 2 or 3.  But few rows (one warp per scheduler or
-// less) leave the SMs idle while a warp does its heads in turn: 42 rows of 32 heads
-// took 10.8 us with W = 1, 6.0 with 2.
+// read meanwhile.  W follows the pieces that the prefix leaves a row (4 over 12, 2
+// over 8); those of its own tokens are not counted, since the host does not know
+// them, so that a row with a long history and little prefix has few warps.  With
+// W = 4 throughout, 256 rows of 32 heads with 7 pieces each took 34 us; a warp per
+// (row, head) took 50 us for 2 000 rows of 32 heads with 2 or 3.  But few rows (one
+// warp per scheduler or less) leave the SMs idle while a warp does its heads in
+// turn: 42 rows of 32 heads took 10.8 us with W = 1, 6.0 with 2.
 constexpr int kMergeWarps = 4;
 constexpr int kFewMergeRows = 4 * 148;
 
@@ -483,11 +486,14 @@ dbsa_status check_paged(const dbsa_config *cfg, const dbsa_paged_cache *cache,
 
 // How many ranges the prefix is cut into: the number for which waves of the CTAs
 // x (key tiles of an item + a piece's own cost) + the partials' traffic is least,
-// with measured costs: a key tile takes a CTA ~1.4 us (32 KB at its share of the
-// memory, or 128 rows' arithmetic at the power limit), starting and ending a piece
-// ~4 us, writing and merging the partials of a row ~0.17 ns x D / 128 of all CTAs'
-// time.  (More, shorter ranges would also even out the SMs' unequal speeds, but
-// behind 90k tokens one row tile takes 69 us with one wave, 75 with two.)
+// with the bf16 kernel's measured costs at D = 128: a key tile takes a CTA ~1.4 us
+// (32 KB at its share of the memory, or 128 rows' arithmetic at the power limit),
+// starting and ending a piece ~4 us, writing and merging the partials of a row
+// ~0.17 ns x D / 128 of all CTAs' time.  fp32 calls are cut by the same costs,
+// although a tile of 64 rows takes a CTA of their kernel ~20 us: they are not split
+// as finely as they could be where they have few key tiles.  (More, shorter ranges
+// would also even out the SMs' unequal speeds, but behind 90k tokens one row tile
+// takes 69 us with one wave, 75 with two.)
 constexpr int kMaxWaves = 8;
 int prefix_groups(int rows, int n_row_tiles, int n_ctas, int Hkv, int D, int64_t units) {
   constexpr double kTile = 1.4, kPiece = 4.0, kRow = 0.17e-3;   // us

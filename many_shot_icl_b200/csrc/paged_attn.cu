@@ -337,7 +337,8 @@ cudaError_t launch_f32(const AttendArgs &a, cudaStream_t st) {
 // are.
 // O is rescaled only when a row's maximum has grown by more than 2^8.
 //
-// Measured (one layer, 32 / 8 heads of 128, prefix of 90 223 tokens): 1 sequence
+// Measured (one layer, 32 / 8 heads of 128, prefix of 90 223 tokens, short runs; back
+// to back at the power limit a call for 64 sequences takes 17 % more): 1 sequence
 // 56 us in this kernel, 370 MB, 6.5 TB/s between its ramps; 64 sequences 105 us,
 // 0.85 PFLOP/s; 64 prompts of ~30 tokens 2.9 ms, 0.97 PFLOP/s at ~2 000 cycles
 // per 128 x 128 scores, where the tensor core alone would take 1 024 with 128-key
@@ -939,7 +940,9 @@ AttendShape attend_shape(const dbsa_config *cfg, int rows, int64_t prefix_len) {
   // fp32: a tile costs what its rows cost, so work that fits one wave of smaller
   // tiles takes those (25 rows x 32 heads behind 71 tokens: 29 us with 64-row
   // tiles).  One more key tile stands for the own tokens, whose lengths the host
-  // does not know; tiles of less than 16 rows would read long ones too often.
+  // does not know (their bound, table_width * page_size, is not used: rows of long
+  // histories behind little prefix get small tiles all the same); tiles of less
+  // than 16 rows would read long ones too often.
   constexpr int least = 16;
   int tile_rows = least;
   const int64_t keys = (prefix_len + kF32Keys - 1) / kF32Keys + 1;
